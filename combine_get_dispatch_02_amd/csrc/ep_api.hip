@@ -4,6 +4,7 @@
 // Validation happens on the host before anything is enqueued, so an invalid
 // call leaves every output untouched and can never make a kernel index out
 // of the buffers described in ep.h.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -449,6 +450,131 @@ int ep_combine(const void* expert_out, int64_t num_rows, const int32_t* token_ro
     return hip_status(ep::launch_combine(expert_out, num_rows, token_row, topk_weights,
                                          num_tokens, hidden, num_topk, combined_x,
                                          static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+// Arguments that ep_route and ep_route_backward share.
+static int check_route(const char* fn, const void* logits, int type, int64_t T, int E, int k, int score,
+                       float scale) {
+    if (T < 0) return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_tokens < 0", fn);
+    if (E < 1) return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_experts < 1", fn);
+    if (E > EP_MAX_EXPERTS) return fail(EP_ERR_UNSUPPORTED, "%s: num_experts > %d", fn, EP_MAX_EXPERTS);
+    if (k < 1) return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_topk < 1", fn);
+    if (k > EP_MAX_TOPK) return fail(EP_ERR_UNSUPPORTED, "%s: num_topk > %d", fn, EP_MAX_TOPK);
+    if (type != EP_TYPE_F32 && type != EP_TYPE_BF16 && type != EP_TYPE_F16)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: unknown logits_type %d", fn, type);
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: unknown score %d", fn, score);
+    if (!isfinite(scale)) return fail(EP_ERR_INVALID_ARGUMENT, "%s: scale is not finite", fn);
+    if (T > INT32_MAX / k) return fail(EP_ERR_UNSUPPORTED, "%s: num_tokens * num_topk >= 2^31", fn);
+    if (T > 0 && !logits) return fail(EP_ERR_INVALID_ARGUMENT, "%s: logits is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(logits) & (type == EP_TYPE_F32 ? 3u : 1u))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: logits must be aligned to its element", fn);
+    return EP_OK;
+}
+
+int ep_route(const void* logits, int logits_type, const float* bias, int64_t num_tokens,
+             int num_experts, int num_topk, int score, int num_groups, int topk_groups,
+             int group_top, int renormalize, float scale, int64_t* topk_idx,
+             float* topk_weights, void* stream) {
+    const char* fn = "ep_route";
+    int s = check_route(fn, logits, logits_type, num_tokens, num_experts, num_topk, score, scale);
+    if (s != EP_OK) return s;
+    if (num_groups < 1 || num_experts % num_groups != 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_experts %% num_groups != 0", fn);
+    if (num_groups > EP_MAX_GROUPS) return fail(EP_ERR_UNSUPPORTED, "%s: num_groups > %d", fn, EP_MAX_GROUPS);
+    if (topk_groups < 1 || topk_groups > num_groups)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: topk_groups outside [1, num_groups]", fn);
+    if (group_top != 1 && group_top != 2) return fail(EP_ERR_INVALID_ARGUMENT, "%s: group_top is 1 or 2", fn);
+    if (num_topk > topk_groups * (num_experts / num_groups))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_topk exceeds the experts of topk_groups groups", fn);
+    if (num_tokens > 0 && (!topk_idx || !topk_weights))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (num_tokens == 0) return EP_OK;
+    const ep::RouteOptions opt = {score == EP_SCORE_SIGMOID, renormalize != 0, scale, num_groups, topk_groups,
+                                  group_top};
+    return hip_status(ep::launch_route(logits, logits_type, bias, num_tokens, num_experts, num_topk, opt,
+                                       topk_idx, topk_weights, static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+int ep_route_backward(const void* logits, int logits_type, const int64_t* topk_idx,
+                      const float* grad_weights, int64_t num_tokens, int num_experts,
+                      int num_topk, int score, int renormalize, float scale, void* grad_logits,
+                      void* stream) {
+    const char* fn = "ep_route_backward";
+    int s = check_route(fn, logits, logits_type, num_tokens, num_experts, num_topk, score, scale);
+    if (s != EP_OK) return s;
+    if (num_tokens > 0 && (!topk_idx || !grad_weights || !grad_logits))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(grad_logits) & (logits_type == EP_TYPE_F32 ? 3u : 1u))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: grad_logits must be aligned to its element", fn);
+    if (num_tokens == 0) return EP_OK;
+    return hip_status(ep::launch_route_backward(logits, logits_type, topk_idx, grad_weights, num_tokens,
+                                                num_experts, num_topk, score == EP_SCORE_SIGMOID,
+                                                renormalize != 0, scale, grad_logits,
+                                                static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+int ep_combine_backward(const void* grad_out, const void* expert_out, int64_t num_rows,
+                        const int32_t* token_row, const float* topk_weights, int64_t num_tokens,
+                        int hidden, int num_topk, void* grad_expert_out,
+                        float* grad_topk_weights, void* stream) {
+    const char* fn = "ep_combine_backward";
+    if (num_tokens < 0 || num_rows < 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_tokens and num_rows must be >= 0", fn);
+    if (num_topk < 1) return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_topk < 1", fn);
+    if (num_topk > EP_MAX_TOPK) return fail(EP_ERR_UNSUPPORTED, "%s: num_topk > %d", fn, EP_MAX_TOPK);
+    if (num_tokens > INT32_MAX / num_topk)
+        return fail(EP_ERR_UNSUPPORTED, "%s: num_tokens * num_topk >= 2^31", fn);
+    if (hidden < 8 || hidden % 8 != 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: hidden must be a positive multiple of 8", fn);
+    if (num_tokens > 0 && num_rows > 0 && !grad_expert_out && !grad_topk_weights)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: grad_expert_out and grad_topk_weights are both NULL", fn);
+    if (num_tokens > 0 && (!grad_out || !token_row))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (num_tokens > 0 && num_rows > 0 && grad_topk_weights && !expert_out)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: expert_out is NULL", fn);
+    if (!aligned16(grad_out) || !aligned16(grad_expert_out) || (grad_topk_weights && !aligned16(expert_out)))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: grad_out, expert_out and grad_expert_out must be 16-byte aligned",
+                    fn);
+    if (num_tokens == 0 || (num_rows == 0 && !grad_topk_weights)) return EP_OK;
+    return hip_status(ep::launch_combine_backward(grad_out, expert_out, num_rows, token_row, topk_weights,
+                                                  num_tokens, hidden, num_topk, grad_expert_out,
+                                                  grad_topk_weights, static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+int ep_expert_linear_w4(const void* x, int64_t num_rows, const int32_t* expert_rows, int capacity,
+                        const uint8_t* w_codes, const uint8_t* w_scales, int num_experts,
+                        int in_features, int out_features, int epilogue, void* y, void* stream) {
+    const char* fn = "ep_expert_linear_w4";
+    if (num_rows < 0 || capacity < 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_rows and capacity must be >= 0", fn);
+    if (num_rows > INT32_MAX) return fail(EP_ERR_UNSUPPORTED, "%s: num_rows >= 2^31", fn);
+    if (num_experts < 1) return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_experts < 1", fn);
+    if (num_experts > EP_MAX_EXPERTS)
+        return fail(EP_ERR_UNSUPPORTED, "%s: num_experts > %d", fn, EP_MAX_EXPERTS);
+    if (capacity > 0 && static_cast<int64_t>(num_experts) * capacity != num_rows)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_rows != num_experts * capacity", fn);
+    if (in_features < 128 || in_features % 128 != 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: in_features must be a positive multiple of 128", fn);
+    if (out_features < 8 || out_features % 8 != 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: out_features must be a positive multiple of 8", fn);
+    if (epilogue != EP_EPILOGUE_NONE && epilogue != EP_EPILOGUE_SILU_MUL)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: unknown epilogue %d", fn, epilogue);
+    if (out_features > INT32_MAX / 2 - 256)
+        return fail(EP_ERR_UNSUPPORTED, "%s: out_features too large", fn);
+    if (num_rows > 0 && (!x || !expert_rows || !w_codes || !w_scales || !y))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (!aligned16(x) || !aligned16(w_codes) || !aligned16(y) || (reinterpret_cast<uintptr_t>(w_scales) & 3u))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: misaligned x / w_codes / w_scales / y", fn);
+    if (num_rows == 0) return EP_OK;
+    return hip_status(ep::launch_expert_linear_w4(x, num_rows, expert_rows, capacity, w_codes, w_scales,
+                                                  num_experts, in_features, out_features,
+                                                  epilogue == EP_EPILOGUE_SILU_MUL, y,
+                                                  static_cast<hipStream_t>(stream)),
                       fn);
 }
 

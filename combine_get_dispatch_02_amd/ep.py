@@ -62,9 +62,15 @@ def lib() -> ctypes.CDLL:
     L.ep_dispatch_ll_workspace_bytes.restype = sz
     L.ep_dispatch_ll.argtypes = [P, P, P, i64, i32, i32, i32, i32, P, P, P, P, P, P, sz, P]
     L.ep_dispatch_ll_fp8.argtypes = [P, P, P, i64, i32, i32, i32, i32, P, P, P, P, P, P, P, sz, P]
+    f32 = ctypes.c_float
+    L.ep_route.argtypes = [P, i32, P, i64, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P]
+    L.ep_route_backward.argtypes = [P, i32, P, P, i64, i32, i32, i32, i32, f32, P, P]
+    L.ep_combine_backward.argtypes = [P, P, i64, P, P, i64, i32, i32, P, P, P]
+    L.ep_expert_linear_w4.argtypes = [P, i64, P, i32, P, P, i32, i32, i32, i32, P, P]
     for f in ("ep_get_dispatch_layout", "ep_dispatch", "ep_dispatch_noalloc", "ep_dispatch_fp8", "ep_combine",
               "ep_dispatch_cached", "ep_dispatch_fp8_cached", "ep_dispatch_ht", "ep_dispatch_ll",
-              "ep_dispatch_ll_fp8"):
+              "ep_dispatch_ll_fp8", "ep_route", "ep_route_backward", "ep_combine_backward",
+              "ep_expert_linear_w4"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -489,6 +495,176 @@ def ep_combine(expert_out: torch.Tensor, token_row: torch.Tensor,
         st = lib().ep_combine(_ptr(expert_out), rows, _ptr(token_row), _ptr(topk_weights), T, H,
                               k, _ptr(out), _stream(dev))
     _check(st, "ep_combine")
+    return out
+
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}      # EP_TYPE_*
+_SCORES = {"softmax": 0, "sigmoid": 1}                                  # EP_SCORE_*
+_EPILOGUES = {"none": 0, "silu_mul": 1}                                 # EP_EPILOGUE_*
+
+
+def _need_logits(logits: torch.Tensor, score: str) -> None:
+    if logits.dtype not in _TYPES:
+        raise TypeError(f"logits must be one of {', '.join(map(str, _TYPES))}, got {logits.dtype}")
+    _need(logits, "logits", logits.dtype)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+
+
+def ep_route(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
+             bias: Optional[torch.Tensor] = None, num_groups: int = 1, topk_groups: int = 1,
+             group_top: int = 2, renormalize: bool = True, scale: float = 1.0,
+             out: Optional[Dict[str, torch.Tensor]] = None) -> Dict[str, torch.Tensor]:
+    """Router logits [T, E] (fp32, bf16 or fp16) to topk_idx [T, k] int64 and
+    topk_weights [T, k] fp32: the k best experts by softmax or sigmoid score
+    plus `bias` [E], out of the topk_groups best of num_groups groups (a
+    group's score is the sum of its group_top best); weights are the scores
+    without the bias, renormalised over the chosen ones if `renormalize`,
+    times `scale`.  Experts whose logit is -inf or NaN are never chosen; where
+    fewer than k are left the slots are empty (-1, weight 0)."""
+    _need_logits(logits, score)
+    dev = logits.device
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", torch.float32, dev)
+        if tuple(bias.shape) != (E,):
+            raise ValueError("bias must be [E]")
+    k = int(num_topk)
+    if out is None:
+        # A bad num_topk is the library's to refuse.
+        out = dict(topk_idx=torch.empty((T, max(k, 0)), dtype=torch.int64, device=dev),
+                   topk_weights=torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev))
+    else:
+        _check_out(out, dev, [("topk_idx", (T, k), torch.int64, True, False),
+                              ("topk_weights", (T, k), torch.float32, True, False)])
+    with torch.cuda.device(dev):
+        st = lib().ep_route(_ptr(logits), _TYPES[logits.dtype], _ptr(bias), T, E, k, _SCORES[score],
+                            num_groups, topk_groups, group_top, int(bool(renormalize)), scale,
+                            _ptr(out["topk_idx"]), _ptr(out["topk_weights"]), _stream(dev))
+    _check(st, "ep_route")
+    return out
+
+
+def ep_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: torch.Tensor, *,
+                      score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of ep_route's topk_weights with respect to the logits: [T, E]
+    in the logits' type, from grad_weights [T, k] fp32 and the topk_idx that
+    ep_route chose.  score, renormalize and scale as in the forward call."""
+    _need_logits(logits, score)
+    dev = logits.device
+    _need(topk_idx, "topk_idx", torch.int64, dev)
+    _need(grad_weights, "grad_weights", torch.float32, dev)
+    T, E = logits.shape
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("logits and topk_idx disagree on num_tokens")
+    if grad_weights.shape != topk_idx.shape:
+        raise ValueError("grad_weights must have the shape of topk_idx")
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _check_out({"out": out}, dev, [("out", (T, E), logits.dtype, True, False)])
+    with torch.cuda.device(dev):
+        st = lib().ep_route_backward(_ptr(logits), _TYPES[logits.dtype], _ptr(topk_idx), _ptr(grad_weights),
+                                     T, E, topk_idx.shape[1], _SCORES[score], int(bool(renormalize)), scale,
+                                     _ptr(out), _stream(dev))
+    _check(st, "ep_route_backward")
+    return out
+
+
+def ep_combine_backward(grad_out: torch.Tensor, expert_out: Optional[torch.Tensor], token_row: torch.Tensor,
+                        topk_weights: Optional[torch.Tensor], num_rows: Optional[int] = None, *,
+                        out: Optional[Dict[str, torch.Tensor]] = None) -> Dict[str, torch.Tensor]:
+    """Gradient of ep_combine: grad_expert_out [num_rows, H] bf16 (rows that no
+    slot maps to are left as they were: uninitialised unless `out` is given)
+    and grad_topk_weights [T, k] fp32 (0 for empty slots).  expert_out None
+    (num_rows is then needed): no grad_topk_weights.  An `out` may hold either
+    of the two alone, and only that one is computed.  Rows have to be distinct,
+    as every dispatch makes them.  The gradient of ep_dispatch is
+    ep_combine(grad_recv_x, token_row, None)."""
+    _need(grad_out, "grad_out", torch.bfloat16)
+    dev = grad_out.device
+    _need(token_row, "token_row", torch.int32, dev)
+    T, H = grad_out.shape
+    if token_row.dim() != 2 or token_row.shape[0] != T:
+        raise ValueError("grad_out and token_row disagree on num_tokens")
+    k = token_row.shape[1]
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, dev)
+        if tuple(topk_weights.shape) != (T, k):
+            raise ValueError("topk_weights must have the shape of token_row")
+    if expert_out is not None:
+        _need(expert_out, "expert_out", torch.bfloat16, dev)
+        if expert_out.dim() != 2 or expert_out.shape[1] != H:
+            raise ValueError("expert_out and grad_out disagree on hidden")
+    elif num_rows is None:
+        raise ValueError("num_rows is needed without expert_out")
+    rows = expert_out.shape[0] if num_rows is None else int(num_rows)
+    if expert_out is not None and rows > expert_out.shape[0]:
+        raise ValueError("num_rows exceeds expert_out rows")
+    if out is None:
+        # A negative num_rows is the library's to refuse.
+        out = dict(grad_expert_out=torch.empty((max(rows, 0), H), dtype=torch.bfloat16, device=dev),
+                   grad_topk_weights=(torch.empty((T, k), dtype=torch.float32, device=dev)
+                                      if expert_out is not None else None))
+    else:
+        _check_out(out, dev, [("grad_expert_out", (rows, H), torch.bfloat16, False, True),
+                              ("grad_topk_weights", (T, k), torch.float32, False, False)])
+        if out.get("grad_topk_weights") is not None and expert_out is None:
+            raise ValueError("grad_topk_weights needs expert_out")
+    with torch.cuda.device(dev):
+        st = lib().ep_combine_backward(_ptr(grad_out), _ptr(expert_out), rows, _ptr(token_row),
+                                       _ptr(topk_weights), T, H, k, _ptr(out.get("grad_expert_out")),
+                                       _ptr(out.get("grad_topk_weights")), _stream(dev))
+    _check(st, "ep_combine_backward")
+    return out
+
+
+def ep_expert_linear_w4(x: torch.Tensor, expert_rows: torch.Tensor, w_codes: torch.Tensor,
+                        w_scales: torch.Tensor, *, capacity: int = 0, epilogue: str = "none",
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The experts' products over dispatched rows with 4-bit weights: y
+    [rows, N] bf16 from x [rows, K] bf16, w_codes [E, W, K/2] uint8 (E2M1, the
+    even input in the low four bits) and w_scales [E, W, K/32] uint8 (E8M0).
+    capacity 0: x is ep_dispatch's recv_x and expert_rows its
+    recv_expert_offset [E+1]; else x is ep_dispatch_ll's recv_x, as
+    [E, capacity, K] or [E*capacity, K], and expert_rows its recv_count [E].
+    epilogue "silu_mul": W = 2N, gate rows first, y = silu(gate) * up; "none":
+    W = N.  Rows of no expert are left as they were (uninitialised unless
+    `out` is given)."""
+    _need(x, "x", torch.bfloat16)
+    dev = x.device
+    _need(expert_rows, "expert_rows", torch.int32, dev)
+    _need(w_codes, "w_codes", torch.uint8, dev)
+    _need(w_scales, "w_scales", torch.uint8, dev)
+    if epilogue not in _EPILOGUES:
+        raise ValueError(f"epilogue must be one of {sorted(_EPILOGUES)}, got {epilogue!r}")
+    if w_codes.dim() != 3 or x.dim() not in ((2, 3) if capacity else (2,)):
+        raise ValueError("x must be [rows, K] (or [E, capacity, K]) and w_codes [E, W, K/2]")
+    E, W = w_codes.shape[:2]
+    K = x.shape[-1]
+    if x.dim() == 3 and tuple(x.shape[:2]) != (E, capacity):
+        raise ValueError("x must be [E, capacity, K]")
+    if w_codes.shape[2] * 2 != K or tuple(w_scales.shape) != (E, W, K // 32):
+        raise ValueError("w_codes must be [E, W, K/2] and w_scales [E, W, K/32]")
+    if tuple(expert_rows.shape) != (E if capacity else E + 1,):
+        raise ValueError("expert_rows must be recv_count [E]" if capacity else
+                         "expert_rows must be recv_expert_offset [E+1]")
+    if epilogue == "silu_mul" and W % 2:
+        raise ValueError("silu_mul needs an even number of weight rows")
+    N = W // 2 if epilogue == "silu_mul" else W
+    shape = (*x.shape[:-1], N)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out({"out": out}, dev, [("out", shape, torch.bfloat16, True, False)])
+    rows = x.shape[0] if x.dim() == 2 else x.shape[0] * x.shape[1]
+    with torch.cuda.device(dev):
+        st = lib().ep_expert_linear_w4(_ptr(x), rows, _ptr(expert_rows), capacity, _ptr(w_codes),
+                                       _ptr(w_scales), E, K, N, _EPILOGUES[epilogue], _ptr(out), _stream(dev))
+    _check(st, "ep_expert_linear_w4")
     return out
 
 

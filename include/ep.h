@@ -324,6 +324,139 @@ int ep_combine(const void* expert_out, int64_t num_rows, const int32_t* token_ro
                const float* topk_weights, int64_t num_tokens, int hidden, int num_topk,
                void* combined_x, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * ep_route -- router logits to the topk_idx / topk_weights that every dispatch
+ * entry point takes.  For each token t:
+ *   score   s[e] = softmax over all E logits, or sigmoid of each logit.
+ *   choice  c[e] = fl32(s[e]) + bias[e] in fp32, where fl32 rounds the score
+ *           from 64 bits.  With bias NULL and either one group or
+ *           group_top == 1 experts are ranked by the logits themselves: the
+ *           order of the exact scores, free of their rounding.
+ *   An expert whose logit or choice is -inf or NaN is unavailable: it is never
+ *   chosen and its softmax term is 0.
+ *   groups  num_groups contiguous blocks of E / num_groups experts.  A group's
+ *           score is the fp32 sum of its group_top (1 or 2) largest available
+ *           choices; only the experts of the topk_groups best groups stay.
+ *   topk_idx[t]  the k largest choices that stay, in descending order.
+ *   topk_weights[t, j] = scale * s[topk_idx[t, j]], divided by the sum of the
+ *           chosen scores if renormalize is not 0.  (The bias only steers the
+ *           choice.)  The division happens before any underflow: scores too
+ *           small for fp32 still renormalise to weights that add to scale.
+ * Ties go to the lowest expert (or group) index.  Where fewer than k experts
+ * are available the remaining slots are empty: topk_idx -1, topk_weights 0 (a
+ * token whose logits are all -inf gets k empty slots, so padding tokens are
+ * dispatched nowhere).  Infinite logits: sigmoid is 1; softmax shares the
+ * whole score equally among a token's +inf logits.
+ *
+ *   logits        [T, E] in, of type logits_type (EP_TYPE_*), aligned to its
+ *                        element
+ *   bias          [E]    fp32  in (may be NULL)
+ *   topk_idx      [T, k] int64 out
+ *   topk_weights  [T, k] fp32  out
+ * Requires T >= 0, 1 <= E <= EP_MAX_EXPERTS, 1 <= k <= EP_MAX_TOPK,
+ * T*k < 2^31, 1 <= num_groups <= EP_MAX_GROUPS, E % num_groups == 0,
+ * 1 <= topk_groups <= num_groups, k <= topk_groups * E / num_groups, a finite
+ * scale.  Outputs must not overlap inputs.  No workspace.
+ *
+ * ep_route_backward -- gradient of topk_weights with respect to the logits
+ * (the choice itself has none, nor has the bias).  With g = grad_weights[t],
+ * s as above and p[j] the renormalised weight (before scale) of slot j:
+ *   softmax, renormalize: d logit += scale * p[j] * (g[j] - sum_i g[i] p[i])
+ *   sigmoid, renormalize: the same times (1 - s)
+ *   sigmoid:              d logit += scale * g[j] * s * (1 - s)
+ *   softmax:              d logit[e] = scale * s[e] * (sum of g[j] over the
+ *                         slots that chose e - sum_i g[i] s[topk_idx[i]])
+ * each added at the expert of slot j, in slot order and in fp32, and rounded
+ * once to the logits' type; every other element is 0.  Empty slots (ids
+ * outside [0, E)) and unavailable logits contribute nothing.
+ *
+ *   topk_idx      [T, k] int64 in (of ep_route; an id may appear twice)
+ *   grad_weights  [T, k] fp32  in
+ *   grad_logits   [T, E] out, of type logits_type
+ * Limits, alignment and overlap as ep_route; no workspace.
+ * ------------------------------------------------------------------------- */
+#define EP_TYPE_F32 0
+#define EP_TYPE_BF16 1
+#define EP_TYPE_F16 2
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+#define EP_MAX_GROUPS 64        /* num_groups of ep_route                     */
+
+int ep_route(const void* logits, int logits_type, const float* bias, int64_t num_tokens,
+             int num_experts, int num_topk, int score, int num_groups, int topk_groups,
+             int group_top, int renormalize, float scale, int64_t* topk_idx,
+             float* topk_weights, void* stream);
+
+int ep_route_backward(const void* logits, int logits_type, const int64_t* topk_idx,
+                      const float* grad_weights, int64_t num_tokens, int num_experts,
+                      int num_topk, int score, int renormalize, float scale, void* grad_logits,
+                      void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ep_combine_backward -- gradient of ep_combine.  With g = grad_out[t], for
+ * every slot (t, j) whose row r = token_row[t, j] lies in [0, num_rows):
+ *   grad_expert_out[r, h]   = bf16(topk_weights[t, j] * g[h])
+ *   grad_topk_weights[t, j] = sum over h of g[h] * expert_out[r, h], in fp32
+ * and grad_topk_weights[t, j] = 0 for every other slot.  Rows that no slot
+ * maps to are not written.  Rows have to be distinct, as every dispatch makes
+ * them: a row that two slots name gets the product of one of them.
+ * (The gradient of ep_dispatch with respect to x is ep_combine over the same
+ * token_row with topk_weights NULL.)
+ *
+ *   grad_out          [T, H]        bf16 in (16-byte aligned)
+ *   expert_out        [num_rows, H] bf16 in (16-byte aligned; may be NULL if
+ *                                   grad_topk_weights is)
+ *   token_row         [T, k]        int32 in
+ *   topk_weights      [T, k]        fp32 in (NULL: all weights 1)
+ *   grad_expert_out   [num_rows, H] bf16 out (16-byte aligned; may be NULL)
+ *   grad_topk_weights [T, k]        fp32 out (may be NULL, but not both)
+ * Requires H % 8 == 0, 1 <= k <= EP_MAX_TOPK, T*k < 2^31, num_rows >= 0.
+ * Outputs must not overlap inputs.  No workspace.
+ * ------------------------------------------------------------------------- */
+int ep_combine_backward(const void* grad_out, const void* expert_out, int64_t num_rows,
+                        const int32_t* token_row, const float* topk_weights, int64_t num_tokens,
+                        int hidden, int num_topk, void* grad_expert_out,
+                        float* grad_topk_weights, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ep_expert_linear_w4 -- the experts' products over dispatched rows, with
+ * 4-bit weights: y[r, n] = sum over i of x[r, i] * W[e, n, i] for every row r
+ * of expert e, accumulated in fp32 and rounded once to bf16.
+ * A weight is an OCP E2M1 code (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives) times the scale 2^(b - 127) of its
+ * group of 32 consecutive inputs (E8M0 byte b; 255 is NaN).  A weight of 2^128
+ * or more (codes 4 and 6 at b >= 253, 2 and 3 too at b = 254) is infinite.
+ *
+ * Rows.  capacity == 0: the packed receive order of ep_dispatch, expert_rows
+ * being recv_expert_offset [E+1] (rows expert_rows[e] .. expert_rows[e+1]-1).
+ * capacity > 0: the padded layout of ep_dispatch_ll, expert_rows being
+ * recv_count [E] (rows e*capacity .. e*capacity + expert_rows[e] - 1) and
+ * num_rows = E*capacity.  Offsets are limited to [0, num_rows] and counts to
+ * [0, capacity], so no map can make the kernel touch rows outside x and y;
+ * rows of no expert are neither read for a result nor written.
+ *
+ * Epilogue.  EP_EPILOGUE_NONE: W has out_features rows.
+ * EP_EPILOGUE_SILU_MUL: W has 2*out_features rows, first the gate's, then the
+ * up projection's, and y = bf16(silu(gate) * up) with gate and up kept in
+ * fp32; silu(v) = v / (1 + exp(-v)).
+ *
+ *   x           [num_rows, in_features]     bf16  in (16-byte aligned)
+ *   expert_rows [E+1] or [E]                int32 in
+ *   w_codes     [E, W rows, in_features/2]  uint8 in (16-byte aligned), two
+ *               codes a byte, the even input in the low four bits
+ *   w_scales    [E, W rows, in_features/32] uint8 in (4-byte aligned)
+ *   y           [num_rows, out_features]    bf16  out (16-byte aligned)
+ * Requires in_features % 128 == 0, out_features % 8 == 0, both positive,
+ * 1 <= E <= EP_MAX_EXPERTS, 0 <= num_rows < 2^31, capacity >= 0.  y must not
+ * overlap the inputs.  No workspace.
+ * ------------------------------------------------------------------------- */
+#define EP_EPILOGUE_NONE 0
+#define EP_EPILOGUE_SILU_MUL 1
+
+int ep_expert_linear_w4(const void* x, int64_t num_rows, const int32_t* expert_rows, int capacity,
+                        const uint8_t* w_codes, const uint8_t* w_scales, int num_experts,
+                        int in_features, int out_features, int epilogue, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
