@@ -560,6 +560,8 @@ int ep_expert_linear_w4(const void* x, int64_t num_rows, const int32_t* expert_r
         return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_rows != num_experts * capacity", fn);
     if (in_features < 128 || in_features % 128 != 0)
         return fail(EP_ERR_INVALID_ARGUMENT, "%s: in_features must be a positive multiple of 128", fn);
+    if (in_features > EP_MAX_IN_FEATURES)
+        return fail(EP_ERR_UNSUPPORTED, "%s: in_features > %d", fn, EP_MAX_IN_FEATURES);
     if (out_features < 8 || out_features % 8 != 0)
         return fail(EP_ERR_INVALID_ARGUMENT, "%s: out_features must be a positive multiple of 8", fn);
     if (epilogue != EP_EPILOGUE_NONE && epilogue != EP_EPILOGUE_SILU_MUL)

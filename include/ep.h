@@ -447,11 +447,13 @@ int ep_combine_backward(const void* grad_out, const void* expert_out, int64_t nu
  *   w_scales    [E, W rows, in_features/32] uint8 in (4-byte aligned)
  *   y           [num_rows, out_features]    bf16  out (16-byte aligned)
  * Requires in_features % 128 == 0, out_features % 8 == 0, both positive,
+ * in_features <= EP_MAX_IN_FEATURES,
  * 1 <= E <= EP_MAX_EXPERTS, 0 <= num_rows < 2^31, capacity >= 0.  y must not
  * overlap the inputs.  No workspace.
  * ------------------------------------------------------------------------- */
 #define EP_EPILOGUE_NONE 0
 #define EP_EPILOGUE_SILU_MUL 1
+#define EP_MAX_IN_FEATURES (1 << 22)
 
 int ep_expert_linear_w4(const void* x, int64_t num_rows, const int32_t* expert_rows, int capacity,
                         const uint8_t* w_codes, const uint8_t* w_scales, int num_experts,

@@ -76,7 +76,7 @@ W4 = dict(x=FAKE, rows=32, erows=FAKE, capacity=0, codes=FAKE, scales=FAKE, E=8,
 
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), EINVAL), (dict(rows=2 ** 31), EUNSUP), (dict(capacity=-1), EINVAL), (dict(capacity=3), EINVAL),
-    (dict(E=0), EINVAL), (dict(E=2049), EUNSUP), (dict(K=64), EINVAL), (dict(K=192), EINVAL), (dict(K=0), EINVAL),
+    (dict(E=0), EINVAL), (dict(E=2049), EUNSUP), (dict(K=64), EINVAL), (dict(K=192), EINVAL), (dict(K=0), EINVAL), (dict(K=2 ** 23), EUNSUP),
     (dict(N=0), EINVAL), (dict(N=12), EINVAL), (dict(N=2 ** 31 - 8), EUNSUP), (dict(epilogue=2), EINVAL),
     (dict(x=None), EINVAL), (dict(erows=None), EINVAL), (dict(codes=None), EINVAL), (dict(scales=None), EINVAL),
     (dict(y=None), EINVAL), (dict(x=ctypes.c_void_p(0x100008)), EINVAL), (dict(codes=ctypes.c_void_p(0x100008)), EINVAL),
