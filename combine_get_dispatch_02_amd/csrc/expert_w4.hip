@@ -22,6 +22,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
+constexpr int kSplitBelow = 2;      // items a block below which its waves split each item
 
 // Eight codes of one word, times the scale 2^(b - 127) whose bits are b << 23.
 __device__ __forceinline__ bf16x8 decode(uint32_t codes, float scale) {
@@ -44,8 +45,20 @@ __device__ __forceinline__ Buffer buffer(const void* p, int64_t bytes) {
 __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane_offset, uint32_t offset) {
     return __builtin_amdgcn_raw_buffer_load_b128(b, lane_offset, __builtin_amdgcn_readfirstlane(offset), 0);
 }
+__device__ __forceinline__ u32x2 load8(Buffer b, uint32_t lane_offset, uint32_t offset) {
+    return __builtin_amdgcn_raw_buffer_load_b64(b, lane_offset, __builtin_amdgcn_readfirstlane(offset), 0);
+}
 __device__ __forceinline__ uint32_t load1(Buffer b, uint32_t lane_offset, uint32_t offset) {
     return __builtin_amdgcn_raw_buffer_load_b8(b, lane_offset, __builtin_amdgcn_readfirstlane(offset), 0);
+}
+
+// 16 bytes a lane past the registers, to the wave's 1024 bytes of shared memory
+// at `to` in lane order.  (The host pass does not know this size.)
+__device__ __forceinline__ void load_shared(u32x4* to, Buffer b, uint32_t lane_offset, uint32_t offset) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, lane_offset,
+                                             __builtin_amdgcn_readfirstlane(offset), 0, 0);
+#endif
 }
 
 struct Rows {
@@ -67,46 +80,72 @@ __device__ __forceinline__ Rows rows_of(const int32_t* __restrict__ expert_rows,
 }
 
 // Work items of a launch, numbered on the device (the row counts are known
-// there only): the row tiles of every expert, expert by expert, and for each
-// the column tiles, which run fastest.  start[e] is the number of row tiles
-// before expert e, limited to int32 (maps out of order could add up to more).
-__device__ void count_tiles(const int32_t* __restrict__ expert_rows, int E, int capacity, int64_t num_rows,
-                            int tile_rows, int32_t* __restrict__ start) {
-    __shared__ int64_t sums[kThreads / kWave];
+// there only): the row tiles of every expert with more than `above` and at most
+// `most` rows, expert by expert, and for each the column tiles, which run
+// fastest.  In shared memory: start[e], the row tiles before expert e (at most
+// INT32_MAX: maps out of order could add up to more), start[E] in all.
+struct Table {
+    int32_t* start;                                 // [E + 1]
+    int32_t* first;                                 // [E] first row
+    int32_t* count;                                 // [E] rows
+};
+size_t table_bytes(int E) { return sizeof(int32_t) * (3 * static_cast<size_t>(E) + 1); }
+
+__device__ __forceinline__ uint32_t add_limited(uint32_t a, uint32_t b) {
+    const uint32_t c = a + b;                       // both at most INT32_MAX
+    return c < INT32_MAX ? c : INT32_MAX;
+}
+
+__device__ Table make_table(int32_t* room, const int32_t* __restrict__ expert_rows, int E, int capacity,
+                            int64_t num_rows, int tile_rows, int above, int most) {
+    __shared__ uint32_t sums[kThreads / kWave];
+    const Table t = {room, room + E + 1, room + 2 * E + 1};
     const int lane = lane_id(), wave = static_cast<int>(threadIdx.x) / kWave;
     const int per = (E + kThreads - 1) / kThreads;
     const int e0 = static_cast<int>(threadIdx.x) * per;
-    int64_t mine = 0;
-    for (int i = 0; i < per; ++i)
-        if (e0 + i < E) mine += (rows_of(expert_rows, e0 + i, capacity, num_rows).count + tile_rows - 1) / tile_rows;
-    int64_t upto = mine;
+    uint32_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = e0 + i;
+        if (e >= E) break;
+        const Rows r = rows_of(expert_rows, e, capacity, num_rows);
+        const int n = r.count > above && r.count <= most ? (r.count - 1) / tile_rows + 1 : 0;
+        t.start[e + 1] = n;                         // summed up below
+        t.first[e] = static_cast<int32_t>(r.first);
+        t.count[e] = r.count;
+        mine = add_limited(mine, n);
+    }
+    uint32_t upto = mine;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
-        const int64_t o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
+        const uint32_t o = __shfl_up(upto, d);
+        if (lane >= d) upto = add_limited(upto, o);
     }
     if (lane == kWave - 1) sums[wave] = upto;
+    uint32_t before = __shfl_up(upto, 1);
+    if (lane == 0) before = 0;
     __syncthreads();
-    int64_t before = upto - mine;
-    for (int w = 0; w < wave; ++w) before += sums[w];
+    for (int w = 0; w < wave; ++w) before = add_limited(before, sums[w]);
+    if (threadIdx.x == 0) t.start[0] = 0;
     for (int i = 0; i < per; ++i) {
         if (e0 + i >= E) break;
-        start[e0 + i] = static_cast<int32_t>(before < INT32_MAX ? before : INT32_MAX);
-        before += (rows_of(expert_rows, e0 + i, capacity, num_rows).count + tile_rows - 1) / tile_rows;
-        if (e0 + i == E - 1) start[E] = static_cast<int32_t>(before < INT32_MAX ? before : INT32_MAX);
+        before = add_limited(before, t.start[e0 + i + 1]);
+        t.start[e0 + i + 1] = before;
     }
     __syncthreads();
+    return t;
 }
 
-// The expert whose row tiles include number `tile` < start[E].
-__device__ __forceinline__ int expert_of(const int32_t* start, int E, int tile) {
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (start[mid] <= tile) lo = mid;
-        else hi = mid;
+// The expert whose row tiles include number `tile` < start[E]: every lane asks
+// about one expert in `step`, then about one of those between.
+__device__ __forceinline__ int expert_of(const Table& t, int E, int tile) {
+    const int step = (E + kWave - 1) / kWave, lane = lane_id();
+    const int p = lane * step;
+    int e = (__popcll(ballot(p < E && t.start[p < E ? p : 0] <= tile)) - 1) * step;
+    if (step > 1) {
+        const int o = e + lane;
+        e += __popcll(ballot(lane < step && o < E && t.start[o < E ? o : 0] <= tile)) - 1;
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(e);
 }
 
 // A launch's share of the items for this block.  Blocks go to the 8 chiplets
@@ -123,117 +162,202 @@ __device__ __forceinline__ Share share_of(int64_t items) {
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
+__device__ __forceinline__ void store4(uint16_t* p, const f32x4& v) {
+    *reinterpret_cast<u32x2*>(p) =
+        u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
+}
+
+// What an item's waves read: weight rows from n0 on (wb[1]: the up rows that
+// belong to them) and token rows from row0 on.
+struct Operands {
+    int64_t row0;
+    int n0, left;                                   // first output, token rows left
+    Buffer wb[2], sb[2], xb;
+};
+template <bool kSilu>
+__device__ __forceinline__ Operands operands(const uint16_t* x, const uint8_t* codes, const uint8_t* scales, int e,
+                                             int64_t row0, int left, int n0, int K, int N) {
+    const int64_t w0 = static_cast<int64_t>(e) * (kSilu ? 2 * N : N) + n0, up = kSilu ? N : 0;
+    const int64_t wide = N - n0 < 256 ? N - n0 : 256, deep = left < 128 ? left : 128;
+    return {row0, n0, left,
+            {buffer(codes + w0 * (K / 2), wide * (K / 2)), buffer(codes + (w0 + up) * (K / 2), wide * (K / 2))},
+            {buffer(scales + w0 * (K / 32), wide * (K / 32)), buffer(scales + (w0 + up) * (K / 32), wide * (K / 32))},
+            buffer(x + row0 * K, deep * K * 2)};
+}
+// Offset of weight row n (of an item's) for a lane of group q.  Rows past the
+// outputs repeat the last one; what they give is not stored.
+__device__ __forceinline__ uint32_t code_offset(const Operands& o, int n, int N, int K, int q) {
+    return static_cast<uint32_t>(o.n0 + n < N ? n : N - 1 - o.n0) * (K / 2) + q * 16;
+}
+
 // ---- few rows per expert: bound by reading the weights ---------------------------
-// One item: up to 16 kRowTiles token rows x 64 weight rows (kSilu: 32 gate rows
-// and their 32 up rows).  The four waves split the inputs, 128 at a time in
-// turn, so that a single token's products still put enough loads in flight, and
-// join their sums in shared memory in wave order.
-template <bool kSilu, int kRowTiles>
-__global__ __launch_bounds__(kThreads, kRowTiles == 1 ? 4 : 2) void stream_w4_kernel(
+// A wave takes 64 weight rows (kSilu: 32 gate rows and their 32 up rows) and up
+// to 32 token rows, 256 inputs at a time: whole 128-byte lines of the codes (64
+// bytes of twice as many rows is a fifth slower from HBM) and, kEven, their eight
+// scales in one load (byte loads cost a quarter of the whole).  Where there are
+// items for every wave, each takes whole items; where there are not (a single
+// token's eight experts), the four waves of a block split an item's inputs, so
+// that every CU has loads in flight, and join their sums in shared memory in wave
+// order.  Nothing is staged: the four waves of a block read the same token rows,
+// which the L1 holds, and never wait for each other.
+
+// acc += the products of kTiles row tiles over inputs k, k + step, ...
+// kEven: K % 256 == 0.
+template <bool kSilu, bool kEven, int kTiles>
+__device__ __forceinline__ void stream_products(const Operands& o, int k, int step, int K, int N, int q, int i16,
+                                                f32x4 (*acc)[4]) {
+    uint32_t cr[4], xr[kTiles];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cr[j] = code_offset(o, (kSilu ? j % 2 : j) * 16 + i16, N, K, q);
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        const int m = i * 16 + i16 < o.left ? i * 16 + i16 : o.left - 1;
+        xr[i] = (static_cast<uint32_t>(m) * K + q * 32) * 2;
+    }
+    u32x4 w[2][2][4], v[2][kTiles][4];              // [buffer][half][weight tile], [half][row tile][..]
+    u32x2 b[2][4];
+    // Every load below is made on every way through the loop, past the end
+    // again from the last block: a branch around a load makes the compiler wait
+    // for all that is on the way.
+    auto load = [&](int buf, int at) {
+        at = at < K ? at : K - 128;
+        const int more = kEven || at + 128 < K ? 128 : 0;
+        if (kEven && at + 128 >= K) at = K - 256;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Buffer wb = o.wb[kSilu ? j / 2 : 0], sb = o.sb[kSilu ? j / 2 : 0];
+            w[buf][0][j] = load16(wb, cr[j], at / 2);
+            w[buf][1][j] = load16(wb, cr[j], (at + more) / 2);
+            if (kEven) {
+                // The line of scales starts where group 0's lane has its own.
+                b[buf][j] = load8(sb, cr[j] / 16 - q, at / 32);
+            } else {
+                b[buf][j][0] = load1(sb, cr[j] / 16, at / 32);
+                b[buf][j][1] = load1(sb, cr[j] / 16, (at + more) / 32);
+            }
+        }
+    };
+    auto rows = [&](int h, int at) {
+        at = at < K ? at : K - 128;
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) v[h][i][s] = load16(o.xb, xr[i], (at + 8 * s) * 2);
+    };
+    auto multiply = [&](int buf, int h) {
+        float scale[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            scale[j] = __uint_as_float((kEven ? b[buf][j][h] >> 8 * q & 0xFF : b[buf][j][h]) << 23);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bf16x8 a = decode(w[buf][h][j][s], scale[j]);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, v[h][i][s]),
+                                                                        acc[i][j], 0, 0, 0);
+            }
+    };
+    // Loads return in order: token rows are asked for before the weights that may
+    // stay on the way while they are waited for.
+    auto pass = [&](int buf, int at) {
+        rows(1, at + 128);
+        __builtin_amdgcn_sched_barrier(0);
+        load(1 - buf, at + step);
+        __builtin_amdgcn_sched_barrier(0);
+        if (at < K) multiply(buf, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        rows(0, at + step);
+        __builtin_amdgcn_sched_barrier(0);
+        if (at + 128 < K) multiply(buf, 1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    load(0, k);
+    rows(0, k);
+    for (; k < K; k += 2 * step) {
+        pass(0, k);
+        pass(1, k + step);
+    }
+}
+
+template <bool kSilu, bool kEven>
+__global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
     const uint16_t* __restrict__ x, int64_t num_rows, const int32_t* __restrict__ expert_rows, int capacity,
-    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N,
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N, int most,
     uint16_t* __restrict__ y) {
     constexpr int kOut = kSilu ? 32 : 64;           // outputs of an item
     __shared__ f32x4 part[4][4][kWave];             // [wave][weight tile][lane]
-    extern __shared__ int32_t start[];              // [E + 1]
+    extern __shared__ int32_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    count_tiles(expert_rows, E, capacity, num_rows, 16 * kRowTiles, start);
+    const Table t = make_table(room, expert_rows, E, capacity, num_rows, 32, 0, most);
     const int columns = (N + kOut - 1) / kOut;
-    const Share mine = share_of(static_cast<int64_t>(start[E]) * columns);
+    const int64_t items = static_cast<int64_t>(t.start[E]) * columns;
+    const bool split = items < kSplitBelow * static_cast<int64_t>(gridDim.x);
+    Share mine = share_of(items);
+    if (!split) {                                   // neighbouring items to the waves of a block
+        mine.at += blockIdx.x / 8 * 3 + wave;
+        mine.step *= 4;
+    }
     for (int64_t item = mine.at; item < mine.end; item += mine.step) {
         const int tile = static_cast<int>(item / columns);
-        const int n0 = static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut;
-        const int e = expert_of(start, E, tile);
-        const Rows rows = rows_of(expert_rows, e, capacity, num_rows);
-        const int m0 = (tile - start[e]) * 16 * kRowTiles, left = rows.count - m0;
+        const int column = static_cast<int>(item - static_cast<int64_t>(tile) * columns);
+        const int e = expert_of(t, E, tile);
+        const int m0 = (tile - t.start[e]) * 32;
+        const int left = __builtin_amdgcn_readfirstlane(t.count[e] - m0);
+        const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
+        const Operands o = operands<kSilu>(x, codes, scales, e, row0, left, column * kOut, K, N);
+        f32x4 acc[2][4] = {};
+        const int k = split ? wave * 256 : 0, step = split ? 1024 : 256;
+        if (left <= 16) stream_products<kSilu, kEven, 1>(o, k, step, K, N, q, i16, acc);
+        else stream_products<kSilu, kEven, 2>(o, k, step, K, N, q, i16, acc);
 
-        // Lanes past the rows or outputs repeat the last one and store nothing.
-        // Addresses: the item's first row, the same in all lanes, and offsets.
-        const int64_t w0 = static_cast<int64_t>(e) * (kSilu ? 2 * N : N) + n0;
-        const int64_t wide = N - n0 < 128 ? N - n0 : 128;
-        const Buffer wb[2] = {buffer(codes + w0 * (K / 2), wide * (K / 2)),
-                              buffer(codes + (w0 + (kSilu ? N : 0)) * (K / 2), wide * (K / 2))};    // [1]: up rows
-        const Buffer sb[2] = {buffer(scales + w0 * (K / 32), wide * (K / 32)),
-                              buffer(scales + (w0 + (kSilu ? N : 0)) * (K / 32), wide * (K / 32))};
-        const Buffer xb = buffer(x + (rows.first + m0) * K, static_cast<int64_t>(left < 128 ? left : 128) * K * 2);
-        uint32_t cr[4], xr[kRowTiles];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            int n = (kSilu ? j % 2 : j) * 16 + i16;
-            n = n0 + n < N ? n : N - 1 - n0;
-            cr[j] = static_cast<uint32_t>(n) * (K / 2) + q * 16;
-        }
+        for (int i = 0; i < 2; ++i) {
+            if (i * 16 >= left) break;
+            // A lane holds outputs 4 q .. + 3 of token row i16 of each 16 x 16
+            // tile; of split items wave w ends up with weight tile w (kSilu: waves
+            // 0 and 1 with the gate's and the up rows').
+            const int m = i * 16 + i16;
+            if (split) {
 #pragma unroll
-        for (int i = 0; i < kRowTiles; ++i) {
-            const int m = i * 16 + i16 < left ? i * 16 + i16 : left - 1;
-            xr[i] = (static_cast<uint32_t>(m) * K + q * 32) * 2;
-        }
-        const int tiles = left < 16 * kRowTiles ? (left + 15) / 16 : kRowTiles;
-
-        f32x4 acc[kRowTiles][4] = {};
-        u32x4 w[2][4];
-        uint32_t b[2][4];
-        auto load = [&](int buf, int kb) {
+                for (int j = 0; j < 4; ++j) part[wave][j][lane] = acc[i][j];
+                __syncthreads();
+                auto sum = [&](int j) {
+                    return (part[0][j][lane] + part[1][j][lane]) + (part[2][j][lane] + part[3][j][lane]);
+                };
+                const int n = o.n0 + wave * 16 + 4 * q;
+                if (wave * 16 < kOut && m < left && n < N) {
+                    f32x4 u = sum(wave);
+                    if (kSilu) {
+                        const f32x4 up = sum(wave + 2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[buf][j] = load16(wb[kSilu ? j / 2 : 0], cr[j], kb / 2);
-                b[buf][j] = load1(sb[kSilu ? j / 2 : 0], cr[j] / 16, kb / 32);
-            }
-        };
-        auto multiply = [&](int buf, int kb) {
+                        for (int c = 0; c < 4; ++c) u[c] = silu(u[c]) * up[c];
+                    }
+                    store4(y + (row0 + m) * N + n, u);
+                }
+                __syncthreads();
+            } else if (m < left) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                bf16x8 a[4];
+                for (int j = 0; j < kOut / 16; ++j) {
+                    const int n = o.n0 + j * 16 + 4 * q;
+                    f32x4 u = acc[i][j];
+                    if (kSilu) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[j] = decode(w[buf][j][s], __uint_as_float(b[buf][j] << 23));
-#pragma unroll
-                for (int i = 0; i < kRowTiles; ++i) {
-                    if (i >= tiles) break;
-                    const bf16x8 v = __builtin_bit_cast(bf16x8, load16(xb, xr[i], (kb + 8 * s) * 2));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], v, acc[i][j], 0, 0, 0);
+                        for (int c = 0; c < 4; ++c) u[c] = silu(u[c]) * acc[i][j + 2][c];
+                    }
+                    if (n < N) store4(y + (row0 + m) * N + n, u);
                 }
             }
-        };
-        int kb = wave * 128;
-        if (kb < K) load(0, kb);
-        for (; kb < K; kb += 1024) {
-            if (kb + 512 < K) load(1, kb + 512);
-            multiply(0, kb);
-            if (kb + 512 >= K) break;
-            if (kb + 1024 < K) load(0, kb + 1024);
-            multiply(1, kb + 512);
-        }
-
-        // Join: thread t takes outputs 4 (t % 16) .. + 3 of token row t / 16.
-        const int m = static_cast<int>(threadIdx.x) / 16, c = static_cast<int>(threadIdx.x) % 16;
-#pragma unroll
-        for (int i = 0; i < kRowTiles; ++i) {
-            if (i >= tiles) break;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[wave][j][lane] = acc[i][j];
-            __syncthreads();
-            auto sum = [&](int j) {
-                const int at = c % 4 * 16 + m;      // the lane that held it
-                return (part[0][j][at] + part[1][j][at]) + (part[2][j][at] + part[3][j][at]);
-            };
-            const int j = c / 4, n = n0 + 4 * c;
-            if (i * 16 + m < left && 4 * c < kOut && n < N) {
-                f32x4 v = sum(j);
-                if (kSilu) {
-                    const f32x4 up = sum(j + 2);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) v[u] = silu(v[u]) * up[u];
-                }
-                *reinterpret_cast<u32x2*>(y + (rows.first + m0 + i * 16 + m) * N + n) =
-                    u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
-            }
-            __syncthreads();
         }
     }
 }
+
+// The 16-byte place in a row of 128 inputs that holds inputs 8 c .. + 7 of row r:
+// rows are read 16 at a time at the same c, which would all meet in one bank.
+__device__ __forceinline__ int place_of(int r, int c) { return c ^ (r & 15); }
 
 // ---- many rows per expert: bound by the matrix unit ------------------------------
 // One item: 128 token rows x 128 weight rows (kSilu: 64 gate rows and their 64
@@ -243,66 +367,51 @@ __global__ __launch_bounds__(kThreads, kRowTiles == 1 ? 4 : 2) void stream_w4_ke
 // the wave that decodes them, a step ahead.
 constexpr int kStep = 128;
 
-// The 16-byte chunk of a 256-byte row that holds inputs 8 c .. + 7 of row r:
-// rows are read 16 at a time at the same c, which would all meet in one bank.
-__device__ __forceinline__ int chunk_of(int r, int c) { return c ^ (r & 15); }
-
 template <bool kSilu>
 __global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
     const uint16_t* __restrict__ x, int64_t num_rows, const int32_t* __restrict__ expert_rows, int capacity,
-    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N,
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N, int above,
     uint16_t* __restrict__ y) {
     constexpr int kOut = kSilu ? 64 : 128;
     __shared__ u32x4 even[128 * 16], odd[128 * 16];
-    extern __shared__ int32_t start[];
+    extern __shared__ int32_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const int wm = wave / 2 * 64, wn = wave % 2;
-    count_tiles(expert_rows, E, capacity, num_rows, 128, start);
+    const Table t = make_table(room, expert_rows, E, capacity, num_rows, 128, above, INT32_MAX);
     const int columns = (N + kOut - 1) / kOut;
-    const Share mine = share_of(static_cast<int64_t>(start[E]) * columns);
+    const Share mine = share_of(static_cast<int64_t>(t.start[E]) * columns);
     for (int64_t item = mine.at; item < mine.end; item += mine.step) {
         const int tile = static_cast<int>(item / columns);
-        const int n0 = static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut;
-        const int e = expert_of(start, E, tile);
-        const Rows rows = rows_of(expert_rows, e, capacity, num_rows);
-        const int m0 = (tile - start[e]) * 128, left = rows.count - m0;
-
-        const int64_t w0 = static_cast<int64_t>(e) * (kSilu ? 2 * N : N) + n0;
-        const int64_t wide = N - n0 < 128 ? N - n0 : 128;
-        const Buffer wb[2] = {buffer(codes + w0 * (K / 2), wide * (K / 2)),
-                              buffer(codes + (w0 + (kSilu ? N : 0)) * (K / 2), wide * (K / 2))};    // [1]: up rows
-        const Buffer sb[2] = {buffer(scales + w0 * (K / 32), wide * (K / 32)),
-                              buffer(scales + (w0 + (kSilu ? N : 0)) * (K / 32), wide * (K / 32))};
-        const Buffer xb = buffer(x + (rows.first + m0) * K, static_cast<int64_t>(left < 128 ? left : 128) * K * 2);
+        const int e = expert_of(t, E, tile);
+        const int m0 = (tile - t.start[e]) * 128;
+        const int left = __builtin_amdgcn_readfirstlane(t.count[e] - m0);
+        const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
+        const Operands o = operands<kSilu>(x, codes, scales, e, row0, left,
+                                           static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut, K, N);
         uint32_t cr[4], fill[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            int n = (kSilu ? wn * 32 + j % 2 * 16 : wn * 64 + j * 16) + i16;
-            n = n0 + n < N ? n : N - 1 - n0;
-            cr[j] = static_cast<uint32_t>(n) * (K / 2) + q * 16;
-        }
+        for (int j = 0; j < 4; ++j)
+            cr[j] = code_offset(o, kSilu ? wn * 32 + j % 2 * 16 + i16 : wn * 64 + j * 16 + i16, N, K, q);
         // This wave fills rows 32 wave .. + 31, four to a load: lane l writes
         // place l % 16 of row l / 16, so it reads the chunk that belongs there.
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = wave * 32 + i * 4 + q;
-            fill[i] = static_cast<uint32_t>(r < left ? r : left - 1) * K * 2 + chunk_of(r, i16) * 16;
+            fill[i] = static_cast<uint32_t>(r < left ? r : left - 1) * K * 2 + place_of(r, i16) * 16;
         }
         auto stage = [&](u32x4* to, int kb) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    xb, (__attribute__((address_space(3))) void*)(to + (wave * 32 + i * 4) * 16), 16, fill[i],
-                    __builtin_amdgcn_readfirstlane(kb * 2), 0, 0);
+                load_shared(to + (wave * 32 + i * 4) * 16, o.xb, fill[i], kb * 2);
         };
         u32x4 w[2][4];
         uint32_t b[2][4];
         auto load = [&](int buf, int kb) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                w[buf][j] = load16(wb[kSilu ? j / 2 : 0], cr[j], kb / 2);
-                b[buf][j] = load1(sb[kSilu ? j / 2 : 0], cr[j] / 16, kb / 32);
+                w[buf][j] = load16(o.wb[kSilu ? j / 2 : 0], cr[j], kb / 2);
+                b[buf][j] = load1(o.sb[kSilu ? j / 2 : 0], cr[j] / 16, kb / 32);
             }
         };
         f32x4 acc[4][4] = {};
@@ -312,7 +421,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = wm + i * 16 + i16;
-                    v[s % 2][i] = __builtin_bit_cast(bf16x8, from[r * 16 + chunk_of(r, q * 4 + s)]);
+                    v[s % 2][i] = __builtin_bit_cast(bf16x8, from[r * 16 + place_of(r, q * 4 + s)]);
                 }
             };
             read(0);
@@ -361,18 +470,16 @@ __global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
         for (int i = 0; i < 4; ++i) {
             const int m = wm + i * 16 + i16;
             if (m >= left) continue;
-            uint16_t* row = y + (rows.first + m0 + m) * N;
+            uint16_t* row = y + (row0 + m) * N;
 #pragma unroll
             for (int j = 0; j < (kSilu ? 2 : 4); ++j) {
-                const int n = n0 + (kSilu ? wn * 32 : wn * 64) + j * 16 + 4 * q;
+                const int n = o.n0 + (kSilu ? wn * 32 : wn * 64) + j * 16 + 4 * q;
                 f32x4 v = acc[i][j];
                 if (kSilu) {
 #pragma unroll
                     for (int u = 0; u < 4; ++u) v[u] = silu(v[u]) * acc[i][j + 2][u];
                 }
-                if (n < N)
-                    *reinterpret_cast<u32x2*>(row + n) =
-                        u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
+                if (n < N) store4(row + n, v);
             }
         }
     }
@@ -396,33 +503,43 @@ unsigned blocks_for(int64_t items, int64_t full) {
     return static_cast<unsigned>((b + 7) / 8 * 8);
 }
 
-template <bool kSilu, int kRowTiles>
-hipError_t launch_stream(const Call& c) {
-    const int64_t tiles = c.num_rows / (16 * kRowTiles) + (c.num_rows < c.E ? c.num_rows : c.E);
-    hipLaunchKernelGGL((stream_w4_kernel<kSilu, kRowTiles>),
-                       dim3(blocks_for(tiles * ceil_div(c.N, kSilu ? 32 : 64), 256 * (kRowTiles == 1 ? 4 : 2))),
-                       dim3(kThreads), sizeof(int32_t) * (c.E + 1), c.stream, static_cast<const uint16_t*>(c.x),
-                       c.num_rows, c.expert_rows, c.capacity, c.codes, c.scales, c.E, c.K, c.N,
-                       static_cast<uint16_t*>(c.y));
+// Row tiles of `rows` that a map in order can ask for at most.
+int64_t most_tiles(const Call& c, int rows) { return c.num_rows / rows + (c.num_rows < c.E ? c.num_rows : c.E); }
+
+template <bool kSilu, bool kEven>
+hipError_t launch_stream(const Call& c, int most) {
+    const int64_t items = most_tiles(c, 32) * ceil_div(c.N, kSilu ? 32 : 64);
+    hipLaunchKernelGGL((stream_w4_kernel<kSilu, kEven>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads),
+                       table_bytes(c.E), c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows,
+                       c.capacity, c.codes, c.scales, c.E, c.K, c.N, most, static_cast<uint16_t*>(c.y));
     return hipGetLastError();
+}
+template <bool kSilu>
+hipError_t launch_stream(const Call& c, int most) {
+    return c.K % 256 == 0 ? launch_stream<kSilu, true>(c, most) : launch_stream<kSilu, false>(c, most);
 }
 
 template <bool kSilu>
-hipError_t launch_tile(const Call& c) {
-    const int64_t tiles = c.num_rows / 128 + (c.num_rows < c.E ? c.num_rows : c.E);
-    hipLaunchKernelGGL((tile_w4_kernel<kSilu>), dim3(blocks_for(tiles * ceil_div(c.N, kSilu ? 64 : 128), 256 * 2)),
-                       dim3(kThreads), sizeof(int32_t) * (c.E + 1), c.stream, static_cast<const uint16_t*>(c.x),
-                       c.num_rows, c.expert_rows, c.capacity, c.codes, c.scales, c.E, c.K, c.N,
-                       static_cast<uint16_t*>(c.y));
+hipError_t launch_tile(const Call& c, int above) {
+    const int64_t items = most_tiles(c, 128) * ceil_div(c.N, kSilu ? 64 : 128);
+    hipLaunchKernelGGL((tile_w4_kernel<kSilu>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads), table_bytes(c.E),
+                       c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows, c.capacity, c.codes,
+                       c.scales, c.E, c.K, c.N, above, static_cast<uint16_t*>(c.y));
     return hipGetLastError();
 }
+
+constexpr int kFew = 32;    // rows of an expert up to which its weights are streamed
 
 template <bool kSilu>
 hipError_t launch(const Call& c) {
-    const int64_t mean = c.num_rows / c.E;
-    if (mean <= 12) return launch_stream<kSilu, 1>(c);
-    if (mean <= 64) return launch_stream<kSilu, 4>(c);
-    return launch_tile<kSilu>(c);
+    // What an expert holds at most (a packed batch: on average).
+    const int64_t rows = c.capacity > 0 ? c.capacity : c.num_rows / c.E;
+    if (rows <= kFew) return launch_stream<kSilu>(c, INT32_MAX);
+    if (c.capacity == 0) return launch_tile<kSilu>(c, 0);
+    // A padded region says little about how many of its rows are filled: each
+    // launch takes the experts that suit it.
+    const hipError_t e = launch_stream<kSilu>(c, kFew);
+    return e != hipSuccess ? e : launch_tile<kSilu>(c, kFew);
 }
 
 }  // namespace
