@@ -48,6 +48,9 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane_offset, uint32_t
 __device__ __forceinline__ u32x2 load8(Buffer b, uint32_t lane_offset, uint32_t offset) {
     return __builtin_amdgcn_raw_buffer_load_b64(b, lane_offset, __builtin_amdgcn_readfirstlane(offset), 0);
 }
+__device__ __forceinline__ uint32_t load4(Buffer b, uint32_t lane_offset, uint32_t offset) {
+    return __builtin_amdgcn_raw_buffer_load_b32(b, lane_offset, __builtin_amdgcn_readfirstlane(offset), 0);
+}
 __device__ __forceinline__ uint32_t load1(Buffer b, uint32_t lane_offset, uint32_t offset) {
     return __builtin_amdgcn_raw_buffer_load_b8(b, lane_offset, __builtin_amdgcn_readfirstlane(offset), 0);
 }
@@ -187,7 +190,7 @@ __device__ __forceinline__ Operands operands(const uint16_t* x, const uint8_t* c
 // Offset of weight row n (of an item's) for a lane of group q.  Rows past the
 // outputs repeat the last one; what they give is not stored.
 __device__ __forceinline__ uint32_t code_offset(const Operands& o, int n, int N, int K, int q) {
-    return static_cast<uint32_t>(o.n0 + n < N ? n : N - 1 - o.n0) * (K / 2) + q * 16;
+    return __umul24(o.n0 + n < N ? n : N - 1 - o.n0, K / 2) + q * 16;
 }
 
 // ---- few rows per expert: bound by reading the weights ---------------------------
@@ -212,7 +215,7 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
         const int m = i * 16 + i16 < o.left ? i * 16 + i16 : o.left - 1;
-        xr[i] = (static_cast<uint32_t>(m) * K + q * 32) * 2;
+        xr[i] = __umul24(m, K * 2) + q * 64;
     }
     u32x4 w[2][2][4], v[2][kTiles][4];              // [buffer][half][weight tile], [half][row tile][..]
     u32x2 b[2][4];
@@ -355,90 +358,100 @@ __global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
     }
 }
 
-// The 16-byte place in a row of 128 inputs that holds inputs 8 c .. + 7 of row r:
-// rows are read 16 at a time at the same c, which would all meet in one bank.
-__device__ __forceinline__ int place_of(int r, int c) { return c ^ (r & 15); }
-
 // ---- many rows per expert: bound by the matrix unit ------------------------------
-// One item: 128 token rows x 128 weight rows (kSilu: 64 gate rows and their 64
-// up rows), 64 x 64 to each of the four waves.  The token rows of a 128-input
-// step come through shared memory (double buffered, loaded past the registers);
-// the codes, an eighth of their bytes per value, straight into the registers of
-// the wave that decodes them, a step ahead.
-constexpr int kStep = 128;
+// One item: 16 kTiles token rows x 256 weight rows (kSilu: 128 gate rows and
+// their 128 up rows), 64 of them to each of the four waves, so that no code is
+// decoded twice.  The token rows of a 128-input step come through shared memory
+// (two buffers, loaded past the registers); the codes go straight into the
+// registers of the wave that decodes them.  Both are asked for a step ahead.
 
-template <bool kSilu>
+// The 16-byte place in a 256-byte row that holds inputs 32 q + 8 s .. + 7 of row
+// r.  A read takes one s, 16 rows and all q; shared memory serves it 16 lanes at
+// a time, of two q's and rows that differ in bits 2 and 3, so those bits of the
+// place must not depend on q.
+__device__ __forceinline__ int place_of(int r, int q, int s) { return (4 * s + q) ^ (r & 15); }
+
+template <bool kSilu, int kTiles>
 __global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
     const uint16_t* __restrict__ x, int64_t num_rows, const int32_t* __restrict__ expert_rows, int capacity,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N, int above,
     uint16_t* __restrict__ y) {
-    constexpr int kOut = kSilu ? 64 : 128;
-    __shared__ u32x4 even[128 * 16], odd[128 * 16];
+    constexpr int kRows = 16 * kTiles, kOut = kSilu ? 128 : 256, kFill = kTiles;
+    __shared__ u32x4 even[kRows * 16], odd[kRows * 16];
     extern __shared__ int32_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const int wm = wave / 2 * 64, wn = wave % 2;
-    const Table t = make_table(room, expert_rows, E, capacity, num_rows, 128, above, INT32_MAX);
+    const Table t = make_table(room, expert_rows, E, capacity, num_rows, kRows, above, INT32_MAX);
     const int columns = (N + kOut - 1) / kOut;
     const Share mine = share_of(static_cast<int64_t>(t.start[E]) * columns);
     for (int64_t item = mine.at; item < mine.end; item += mine.step) {
         const int tile = static_cast<int>(item / columns);
         const int e = expert_of(t, E, tile);
-        const int m0 = (tile - t.start[e]) * 128;
+        const int m0 = (tile - t.start[e]) * kRows;
         const int left = __builtin_amdgcn_readfirstlane(t.count[e] - m0);
         const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
         const Operands o = operands<kSilu>(x, codes, scales, e, row0, left,
                                            static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut, K, N);
-        uint32_t cr[4], fill[8];
+        uint32_t cr[4], fill[kFill];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            cr[j] = code_offset(o, kSilu ? wn * 32 + j % 2 * 16 + i16 : wn * 64 + j * 16 + i16, N, K, q);
-        // This wave fills rows 32 wave .. + 31, four to a load: lane l writes
-        // place l % 16 of row l / 16, so it reads the chunk that belongs there.
+            cr[j] = code_offset(o, kSilu ? wave * 32 + j % 2 * 16 + i16 : wave * 64 + j * 16 + i16, N, K, q);
+        // This wave fills rows 4 kTiles wave .. on, four to a load: lane l writes
+        // place l % 16 of row l / 16, so it reads the inputs that belong there.
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = wave * 32 + i * 4 + q;
-            fill[i] = static_cast<uint32_t>(r < left ? r : left - 1) * K * 2 + place_of(r, i16) * 16;
+        for (int i = 0; i < kFill; ++i) {
+            const int r = wave * 4 * kTiles + i * 4 + q, c = i16 ^ (r & 15);
+            fill[i] = __umul24(r < left ? r : left - 1, K * 2) + (c % 4) * 64 + (c / 4) * 16;
         }
         auto stage = [&](u32x4* to, int kb) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                load_shared(to + (wave * 32 + i * 4) * 16, o.xb, fill[i], kb * 2);
+            for (int i = 0; i < kFill; ++i)
+                load_shared(to + (wave * 4 * kTiles + i * 4) * 16, o.xb, fill[i], kb * 2);
         };
         u32x4 w[2][4];
-        uint32_t b[2][4];
+        uint32_t b[2][4];                           // the four scales of 128 inputs
         auto load = [&](int buf, int kb) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 w[buf][j] = load16(o.wb[kSilu ? j / 2 : 0], cr[j], kb / 2);
-                b[buf][j] = load1(o.sb[kSilu ? j / 2 : 0], cr[j] / 16, kb / 32);
+                b[buf][j] = load4(o.sb[kSilu ? j / 2 : 0], cr[j] / 16 - q, kb / 32);
             }
         };
-        f32x4 acc[4][4] = {};
+        f32x4 acc[kTiles][4] = {};
         auto multiply = [&](const u32x4* from, int buf) {
-            bf16x8 v[2][4];
-            auto read = [&](int s) {
+            float scale[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = wm + i * 16 + i16;
-                    v[s % 2][i] = __builtin_bit_cast(bf16x8, from[r * 16 + place_of(r, q * 4 + s)]);
-                }
+            for (int j = 0; j < 4; ++j) scale[j] = __uint_as_float((b[buf][j] >> 8 * q & 0xFF) << 23);
+            bf16x8 v[kTiles], a[2];
+            // Place 4 s + q of row 16 i + i16, exclusive-or i16 (place_of): worked out
+            // anew from one register, which the compiler may not see through, or
+            // it keeps one for every s.
+            int first = i16 * 16 + place_of(i16, q, 0);
+            asm("" : "+v"(first));
+            auto read = [&](int i, int s) {
+                v[i] = __builtin_bit_cast(bf16x8, from[i * 256 + (first ^ 4 * s)]);
             };
-            read(0);
-            // The barriers to scheduling keep each step's reads ahead of the
-            // products of the step before, and no further: all four in front spill.
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (s < 3) read(s + 1);
-                __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < kTiles; ++i) read(i, 0);
+            a[0] = decode(w[buf][0][0], scale[0]);
+            // Each weight tile is decoded beside the products of the one before,
+            // and the next inputs of a row tile read when its last product is
+            // under way.  The barriers to scheduling keep it that way: left
+            // alone, all reads and decodes move to the front and spill.
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const bf16x8 a = decode(w[buf][j][s], __uint_as_float(b[buf][j] << 23));
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (j < 3) a[(j + 1) % 2] = decode(w[buf][j + 1][s], scale[j + 1]);
+                    else if (s < 3) a[0] = decode(w[buf][0][s + 1], scale[0]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v[s % 2][i], acc[i][j], 0, 0, 0);
+                    for (int i = 0; i < kTiles; ++i) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j % 2], v[i], acc[i][j], 0, 0, 0);
+                        if (j == 3 && s < 3) read(i, s + 1);
+                    }
                 }
-            }
+            __builtin_amdgcn_sched_barrier(0);
         };
         // A step's loads have arrived (vmcnt), in every wave (barrier), and every
         // wave is done with the step before, whose buffer the next loads fill.
@@ -446,34 +459,36 @@ __global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             __syncthreads();
         };
+        // No branch in the loop: past the end the last step is asked for again.
         __syncthreads();                            // the last item's reads are done
         stage(even, 0);
         load(0, 0);
-        for (int kb = 0; kb < K; kb += 2 * kStep) {
+        int kb = 0;
+        for (; kb + 256 <= K; kb += 256) {
             arrive();
-            if (kb + kStep < K) {
-                stage(odd, kb + kStep);
-                load(1, kb + kStep);
-            }
+            stage(odd, kb + 128);
+            load(1, kb + 128);
             multiply(even, 0);
-            if (kb + kStep >= K) break;
             arrive();
-            if (kb + 2 * kStep < K) {
-                stage(even, kb + 2 * kStep);
-                load(0, kb + 2 * kStep);
-            }
+            const int next = kb + 256 < K ? kb + 256 : K - 128;
+            stage(even, next);
+            load(0, next);
             multiply(odd, 1);
+        }
+        if (kb < K) {
+            arrive();
+            multiply(even, 0);
         }
 
         // A lane holds outputs 4 q .. + 3 of token row i16 of each 16 x 16 tile.
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = wm + i * 16 + i16;
-            if (m >= left) continue;
+        for (int i = 0; i < kTiles; ++i) {
+            const int m = i * 16 + i16;
+            if (m >= left) break;
             uint16_t* row = y + (row0 + m) * N;
 #pragma unroll
             for (int j = 0; j < (kSilu ? 2 : 4); ++j) {
-                const int n = o.n0 + (kSilu ? wn * 32 : wn * 64) + j * 16 + 4 * q;
+                const int n = o.n0 + wave * (kSilu ? 32 : 64) + j * 16 + 4 * q;
                 f32x4 v = acc[i][j];
                 if (kSilu) {
 #pragma unroll
@@ -519,15 +534,16 @@ hipError_t launch_stream(const Call& c, int most) {
     return c.K % 256 == 0 ? launch_stream<kSilu, true>(c, most) : launch_stream<kSilu, false>(c, most);
 }
 
-template <bool kSilu>
+template <bool kSilu, int kTiles>
 hipError_t launch_tile(const Call& c, int above) {
-    const int64_t items = most_tiles(c, 128) * ceil_div(c.N, kSilu ? 64 : 128);
-    hipLaunchKernelGGL((tile_w4_kernel<kSilu>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads), table_bytes(c.E),
-                       c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows, c.capacity, c.codes,
-                       c.scales, c.E, c.K, c.N, above, static_cast<uint16_t*>(c.y));
+    const int64_t items = most_tiles(c, 16 * kTiles) * ceil_div(c.N, kSilu ? 128 : 256);
+    hipLaunchKernelGGL((tile_w4_kernel<kSilu, kTiles>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads),
+                       table_bytes(c.E), c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows,
+                       c.capacity, c.codes, c.scales, c.E, c.K, c.N, above, static_cast<uint16_t*>(c.y));
     return hipGetLastError();
 }
 
+constexpr int kSmallTile = 96;
 constexpr int kFew = 32;    // rows of an expert up to which its weights are streamed
 
 template <bool kSilu>
@@ -535,11 +551,11 @@ hipError_t launch(const Call& c) {
     // What an expert holds at most (a packed batch: on average).
     const int64_t rows = c.capacity > 0 ? c.capacity : c.num_rows / c.E;
     if (rows <= kFew) return launch_stream<kSilu>(c, INT32_MAX);
-    if (c.capacity == 0) return launch_tile<kSilu>(c, 0);
+    if (c.capacity == 0) return rows <= kSmallTile ? launch_tile<kSilu, 4>(c, 0) : launch_tile<kSilu, 8>(c, 0);
     // A padded region says little about how many of its rows are filled: each
     // launch takes the experts that suit it.
     const hipError_t e = launch_stream<kSilu>(c, kFew);
-    return e != hipSuccess ? e : launch_tile<kSilu>(c, kFew);
+    return e != hipSuccess ? e : launch_tile<kSilu, 8>(c, kFew);
 }
 
 }  // namespace
