@@ -20,6 +20,7 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
 constexpr int kSplitBelow = 2;      // items a block below which its waves split each item
@@ -163,7 +164,11 @@ __device__ __forceinline__ Share share_of(int64_t items) {
     return {items * xcd / 8 + blockIdx.x / 8, items * (xcd + 1) / 8, static_cast<int64_t>(gridDim.x) / 8};
 }
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// v / (1 + exp(-v)) by the hardware's 2^x and reciprocal, each off by a step or
+// so of fp32: |v| of them in all, where half a step of the result's bf16 is 2^15.
+__device__ __forceinline__ float silu(float v) {
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
+}
 
 __device__ __forceinline__ void store4(uint16_t* p, const f32x4& v) {
     *reinterpret_cast<u32x2*>(p) =
@@ -359,27 +364,32 @@ __global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
 }
 
 // ---- many rows per expert: bound by the matrix unit ------------------------------
-// One item: 16 kTiles token rows x 256 weight rows (kSilu: 128 gate rows and
+// One item: 32 kTiles token rows x 256 weight rows (kSilu: 128 gate rows and
 // their 128 up rows), 64 of them to each of the four waves, so that no code is
 // decoded twice.  The token rows of a 128-input step come through shared memory
 // (two buffers, loaded past the registers); the codes go straight into the
 // registers of the wave that decodes them.  Both are asked for a step ahead.
 
-// The 16-byte place in a 256-byte row that holds inputs 32 q + 8 s .. + 7 of row
-// r.  A read takes one s, 16 rows and all q; shared memory serves it 16 lanes at
-// a time, of two q's and rows that differ in bits 2 and 3, so those bits of the
-// place must not depend on q.
-__device__ __forceinline__ int place_of(int r, int q, int s) { return (4 * s + q) ^ (r & 15); }
+// Products are 32 x 32 here (v_mfma_f32_32x32x16_bf16): per operation they read
+// half the operand registers of the 16 x 16 form, and at these sizes the card's
+// power bounds the clock.  A lane holds row lane % 32 of either operand; its half
+// h = lane / 32 holds 8 of the 16 inputs.  Two loads bring a lane the codes of
+// groups h and 2 + h of a 128-input step; step (u, s) of eight contracts inputs
+// 32 (2 u + h) + 8 s .. + 7.
+
+// The 16-byte place in a 256-byte row that holds inputs 8 c .. + 7 of row r.
+// Shared memory serves 16 lanes at a time, of 16 different rows mod 16.
+__device__ __forceinline__ int place_of(int r, int c) { return c ^ (r & 15); }
 
 template <bool kSilu, int kTiles>
 __global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
     const uint16_t* __restrict__ x, int64_t num_rows, const int32_t* __restrict__ expert_rows, int capacity,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N, int above,
     uint16_t* __restrict__ y) {
-    constexpr int kRows = 16 * kTiles, kOut = kSilu ? 128 : 256, kFill = kTiles;
+    constexpr int kRows = 32 * kTiles, kOut = kSilu ? 128 : 256, kFill = 2 * kTiles;
     __shared__ u32x4 even[kRows * 16], odd[kRows * 16];
     extern __shared__ int32_t room[];
-    const int lane = lane_id(), q = lane / 16, i16 = lane % 16;
+    const int lane = lane_id(), h = lane / 32, i32 = lane % 32;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const Table t = make_table(room, expert_rows, E, capacity, num_rows, kRows, above, INT32_MAX);
     const int columns = (N + kOut - 1) / kOut;
@@ -392,63 +402,68 @@ __global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
         const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
         const Operands o = operands<kSilu>(x, codes, scales, e, row0, left,
                                            static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut, K, N);
-        uint32_t cr[4], fill[kFill];
+        uint32_t cr[2], fill[kFill];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            cr[j] = code_offset(o, kSilu ? wave * 32 + j % 2 * 16 + i16 : wave * 64 + j * 16 + i16, N, K, q);
-        // This wave fills rows 4 kTiles wave .. on, four to a load: lane l writes
+        for (int j = 0; j < 2; ++j)
+            cr[j] = code_offset(o, kSilu ? wave * 32 + i32 : wave * 64 + j * 32 + i32, N, K, h);
+        // This wave fills rows 8 kTiles wave .. on, four to a load: lane l writes
         // place l % 16 of row l / 16, so it reads the inputs that belong there.
 #pragma unroll
         for (int i = 0; i < kFill; ++i) {
-            const int r = wave * 4 * kTiles + i * 4 + q, c = i16 ^ (r & 15);
-            fill[i] = __umul24(r < left ? r : left - 1, K * 2) + (c % 4) * 64 + (c / 4) * 16;
+            const int r = wave * 8 * kTiles + i * 4 + lane / 16;
+            fill[i] = __umul24(r < left ? r : left - 1, K * 2) + place_of(r, lane % 16) * 16;
         }
         auto stage = [&](u32x4* to, int kb) {
 #pragma unroll
             for (int i = 0; i < kFill; ++i)
-                load_shared(to + (wave * 4 * kTiles + i * 4) * 16, o.xb, fill[i], kb * 2);
+                load_shared(to + (wave * 8 * kTiles + i * 4) * 16, o.xb, fill[i], kb * 2);
         };
-        u32x4 w[2][4];
-        uint32_t b[2][4];                           // the four scales of 128 inputs
+        u32x4 w[2][2][2];                           // [buffer][weight tile][u]
+        uint32_t b[2][2];                           // the four scales of 128 inputs
         auto load = [&](int buf, int kb) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[buf][j] = load16(o.wb[kSilu ? j / 2 : 0], cr[j], kb / 2);
-                b[buf][j] = load4(o.sb[kSilu ? j / 2 : 0], cr[j] / 16 - q, kb / 32);
+            for (int j = 0; j < 2; ++j) {
+                w[buf][j][0] = load16(o.wb[kSilu ? j : 0], cr[j], kb / 2);
+                w[buf][j][1] = load16(o.wb[kSilu ? j : 0], cr[j], kb / 2 + 32);
+                b[buf][j] = load4(o.sb[kSilu ? j : 0], cr[j] / 16 - h, kb / 32);
             }
         };
-        f32x4 acc[kTiles][4] = {};
+        f32x16 acc[kTiles][2] = {};
         auto multiply = [&](const u32x4* from, int buf) {
-            float scale[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) scale[j] = __uint_as_float((b[buf][j] >> 8 * q & 0xFF) << 23);
             bf16x8 v[kTiles], a[2];
-            // Place 4 s + q of row 16 i + i16, exclusive-or i16 (place_of): worked out
-            // anew from one register, which the compiler may not see through, or
-            // it keeps one for every s.
-            int first = i16 * 16 + place_of(i16, q, 0);
+            // Place 4 h of row i32, from which the others differ by an exclusive or:
+            // worked out anew from one register, which the compiler may not see
+            // through, or it keeps one for every place.
+            int first = i32 * 16 + place_of(i32, 4 * h);
             asm("" : "+v"(first));
-            auto read = [&](int i, int s) {
-                v[i] = __builtin_bit_cast(bf16x8, from[i * 256 + (first ^ 4 * s)]);
+            auto read = [&](int i, int us) {
+                v[i] = __builtin_bit_cast(bf16x8, from[i * 512 + (first ^ ((us & 4) * 2 + us % 4))]);
+            };
+            auto decode_tile = [&](int j, int us) {
+                const uint32_t scale = (b[buf][j] >> (8 * h + 16 * (us / 4)) & 0xFF) << 23;
+                return decode(w[buf][j][us / 4][us % 4], __uint_as_float(scale));
             };
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) read(i, 0);
-            a[0] = decode(w[buf][0][0], scale[0]);
+            a[0] = decode_tile(0, 0);
             // Each weight tile is decoded beside the products of the one before,
             // and the next inputs of a row tile read when its last product is
             // under way.  The barriers to scheduling keep it that way: left
             // alone, all reads and decodes move to the front and spill.
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int us = 0; us < 8; ++us)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 2; ++j) {
                     __builtin_amdgcn_sched_barrier(0);
-                    if (j < 3) a[(j + 1) % 2] = decode(w[buf][j + 1][s], scale[j + 1]);
-                    else if (s < 3) a[0] = decode(w[buf][0][s + 1], scale[0]);
+                    if (j == 0) a[1] = decode_tile(1, us);
+                    else if (us < 7) a[0] = decode_tile(0, us + 1);
 #pragma unroll
                     for (int i = 0; i < kTiles; ++i) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j % 2], v[i], acc[i][j], 0, 0, 0);
-                        if (j == 3 && s < 3) read(i, s + 1);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[j], v[i], acc[i][j], 0, 0, 0);
+                        if (j == 1 && us < 7) {
+                            read(i, us + 1);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
                     }
                 }
             __builtin_amdgcn_sched_barrier(0);
@@ -480,22 +495,26 @@ __global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
             multiply(even, 0);
         }
 
-        // A lane holds outputs 4 q .. + 3 of token row i16 of each 16 x 16 tile.
+        // A lane holds outputs 8 p + 4 h .. + 3 (p = 0 .. 3) of token row i32 of
+        // each 32 x 32 tile.
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-            const int m = i * 16 + i16;
+            const int m = i * 32 + i32;
             if (m >= left) break;
             uint16_t* row = y + (row0 + m) * N;
 #pragma unroll
-            for (int j = 0; j < (kSilu ? 2 : 4); ++j) {
-                const int n = o.n0 + wave * (kSilu ? 32 : 64) + j * 16 + 4 * q;
-                f32x4 v = acc[i][j];
-                if (kSilu) {
+            for (int j = 0; j < (kSilu ? 1 : 2); ++j)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) v[u] = silu(v[u]) * acc[i][j + 2][u];
+                for (int p = 0; p < 4; ++p) {
+                    const int n = o.n0 + wave * (kSilu ? 32 : 64) + j * 32 + 8 * p + 4 * h;
+                    f32x4 v;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        v[c] = acc[i][j][4 * p + c];
+                        if (kSilu) v[c] = silu(v[c]) * acc[i][1][4 * p + c];
+                    }
+                    if (n < N) store4(row + n, v);
                 }
-                if (n < N) store4(row + n, v);
-            }
         }
     }
 }
@@ -536,7 +555,7 @@ hipError_t launch_stream(const Call& c, int most) {
 
 template <bool kSilu, int kTiles>
 hipError_t launch_tile(const Call& c, int above) {
-    const int64_t items = most_tiles(c, 16 * kTiles) * ceil_div(c.N, kSilu ? 128 : 256);
+    const int64_t items = most_tiles(c, 32 * kTiles) * ceil_div(c.N, kSilu ? 128 : 256);
     hipLaunchKernelGGL((tile_w4_kernel<kSilu, kTiles>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads),
                        table_bytes(c.E), c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows,
                        c.capacity, c.codes, c.scales, c.E, c.K, c.N, above, static_cast<uint16_t*>(c.y));
@@ -551,11 +570,11 @@ hipError_t launch(const Call& c) {
     // What an expert holds at most (a packed batch: on average).
     const int64_t rows = c.capacity > 0 ? c.capacity : c.num_rows / c.E;
     if (rows <= kFew) return launch_stream<kSilu>(c, INT32_MAX);
-    if (c.capacity == 0) return rows <= kSmallTile ? launch_tile<kSilu, 4>(c, 0) : launch_tile<kSilu, 8>(c, 0);
+    if (c.capacity == 0) return rows <= kSmallTile ? launch_tile<kSilu, 2>(c, 0) : launch_tile<kSilu, 4>(c, 0);
     // A padded region says little about how many of its rows are filled: each
     // launch takes the experts that suit it.
     const hipError_t e = launch_stream<kSilu>(c, kFew);
-    return e != hipSuccess ? e : launch_tile<kSilu, 8>(c, kFew);
+    return e != hipSuccess ? e : launch_tile<kSilu, 4>(c, kFew);
 }
 
 }  // namespace
