@@ -23,6 +23,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
+constexpr int kTileRows = 128, kTileWeights = 512, kTileThreads = 512;
 constexpr int kSplitBelow = 2;      // items a block below which its waves split each item
 
 // Eight codes of one word, times the scale 2^(b - 127) whose bits are b << 23.
@@ -102,10 +103,10 @@ __device__ __forceinline__ uint32_t add_limited(uint32_t a, uint32_t b) {
 
 __device__ Table make_table(int32_t* room, const int32_t* __restrict__ expert_rows, int E, int capacity,
                             int64_t num_rows, int tile_rows, int above, int most) {
-    __shared__ uint32_t sums[kThreads / kWave];
+    __shared__ uint32_t sums[8];
     const Table t = {room, room + E + 1, room + 2 * E + 1};
     const int lane = lane_id(), wave = static_cast<int>(threadIdx.x) / kWave;
-    const int per = (E + kThreads - 1) / kThreads;
+    const int threads = static_cast<int>(blockDim.x), per = (E + threads - 1) / threads;
     const int e0 = static_cast<int>(threadIdx.x) * per;
     uint32_t mine = 0;
     for (int i = 0; i < per; ++i) {
@@ -186,7 +187,7 @@ template <bool kSilu>
 __device__ __forceinline__ Operands operands(const uint16_t* x, const uint8_t* codes, const uint8_t* scales, int e,
                                              int64_t row0, int left, int n0, int K, int N) {
     const int64_t w0 = static_cast<int64_t>(e) * (kSilu ? 2 * N : N) + n0, up = kSilu ? N : 0;
-    const int64_t wide = N - n0 < 256 ? N - n0 : 256, deep = left < 128 ? left : 128;
+    const int64_t wide = N - n0 < 512 ? N - n0 : 512, deep = left < 128 ? left : 128;
     return {row0, n0, left,
             {buffer(codes + w0 * (K / 2), wide * (K / 2)), buffer(codes + (w0 + up) * (K / 2), wide * (K / 2))},
             {buffer(scales + w0 * (K / 32), wide * (K / 32)), buffer(scales + (w0 + up) * (K / 32), wide * (K / 32))},
@@ -377,145 +378,173 @@ __global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
 // groups h and 2 + h of a 128-input step; step (u, s) of eight contracts inputs
 // 32 (2 u + h) + 8 s .. + 7.
 
+// The loads behind the newest kLater have arrived in every wave, and every wave
+// is done with the shared memory it read.
+template <int kLater>
+__device__ __forceinline__ void arrive() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLater) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // The 16-byte place in a 256-byte row that holds inputs 8 c .. + 7 of row r.
 // Shared memory serves 16 lanes at a time, of 16 different rows mod 16.
 __device__ __forceinline__ int place_of(int r, int c) { return c ^ (r & 15); }
 
+// One item: up to 32 kTiles token rows.
 template <bool kSilu, int kTiles>
-__global__ __launch_bounds__(kThreads, 2) void tile_w4_kernel(
+__device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint16_t* __restrict__ y, u32x4* s0,
+                                          u32x4* s1, u32x4* s2, u32x4* s3) {
+    constexpr int kFill = kTiles;                   // loads of four rows a wave
+    const int lane = lane_id(), h = lane / 32, i32 = lane % 32;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+    uint32_t cr[2], fill[kFill];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        cr[j] = code_offset(o, kSilu ? wave * 32 + i32 : wave * 64 + j * 32 + i32, N, K, h);
+    // This wave fills rows 4 kFill wave .. on, four to a load: lane l writes
+    // place l % 16 of row l / 16, so it reads the inputs that belong there.
+#pragma unroll
+    for (int i = 0; i < kFill; ++i) {
+        const int r = (wave * kFill + i) * 4 + lane / 16;
+        fill[i] = __umul24(r < o.left ? r : o.left - 1, K * 2) + place_of(r, lane % 16) * 16;
+    }
+    u32x4 w[2][2][2];                           // [buffer][weight tile][u]
+    uint32_t b[2][2];                           // the four scales of 128 inputs
+    // Load number g of the six of a step's weights, and of its token rows.
+    auto ask_weights = [&](int g, int buf, int kb) {
+        const int j = g / 3, u = g % 3;
+        if (u == 2) b[buf][j] = load4(o.sb[kSilu ? j : 0], cr[j] / 16 - h, kb / 32);
+        else w[buf][j][u] = load16(o.wb[kSilu ? j : 0], cr[j], kb / 2 + 32 * u);
+    };
+    auto ask_rows = [&](int g, u32x4* to, int kb) {
+        load_shared(to + (wave * kFill + g) * 64, o.xb, fill[g], kb * 2);
+    };
+    // Past the end the last step is asked for again.
+    auto within = [&](int kb) { return kb < K ? kb : K - 128; };
+    f32x16 acc[kTiles][2] = {};
+    bf16x8 v[kTiles], a[2];
+    auto read = [&](const u32x4* from, int first, int i, int us) {
+        v[i] = __builtin_bit_cast(bf16x8, from[i * 512 + (first ^ ((us & 4) * 2 + us % 4))]);
+    };
+    auto decode_tile = [&](int buf, int j, int us) {
+        const uint32_t scale = (b[buf][j] >> (8 * h + 16 * (us / 4)) & 0xFF) << 23;
+        return decode(w[buf][j][us / 4][us % 4], __uint_as_float(scale));
+    };
+    // The products of the step at kb, in 16 groups.  Between the groups its
+    // loads are asked for, one at a time (all at once they hold up the
+    // wave's products): first the weights of the next step, and in the
+    // second half the token rows of the third next.  The barrier in the
+    // middle says that the next step's rows, asked for two steps ago, are in
+    // (behind them are at most one step's rows and weights: the vmcnt), and
+    // that every wave is past the step before, whose rows are overwritten.
+    // So no wave waits for memory at a barrier.  Each weight tile is decoded
+    // beside the products of the one before; the next inputs of a row tile
+    // are read when its last product is under way.  The barriers to
+    // scheduling keep all that in place.
+    auto multiply = [&](const u32x4* from, const u32x4* then, u32x4* to, int buf, int kb) {
+        // Place 4 h of row i32, from which the others differ by an exclusive or:
+        // worked out anew from one register, which the compiler may not see
+        // through, or it keeps one for every place.
+        int first = i32 * 16 + place_of(i32, 4 * h);
+        asm("" : "+v"(first));
+#pragma unroll
+        for (int us = 0; us < 8; ++us)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int group = us * 2 + j;
+                __builtin_amdgcn_sched_barrier(0);
+                if (group < 6) ask_weights(group, 1 - buf, within(kb + 128));
+                if (group == 8) arrive<6 + kFill>();
+                if (group > 8 && group - 9 < kFill) ask_rows(group - 9, to, within(kb + 384));
+                __builtin_amdgcn_sched_barrier(0);
+                if (j == 0) a[1] = decode_tile(buf, 1, us);
+                else if (us < 7) a[0] = decode_tile(buf, 0, us + 1);
+                else a[0] = decode_tile(1 - buf, 0, 0);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[j], v[i], acc[i][j], 0, 0, 0);
+                    if (j == 1) {
+                        if (us < 7) read(from, first, i, us + 1);
+                        else read(then, first, i, 0);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+    };
+    static_assert(kFill <= 7, "rows are asked for in the last seven groups");
+    arrive<0>();                                // the last item's loads and reads are done
+#pragma unroll
+    for (int g = 0; g < 6; ++g) ask_weights(g, 0, 0);
+#pragma unroll
+    for (int g = 0; g < kFill; ++g) ask_rows(g, s0, 0);
+#pragma unroll
+    for (int g = 0; g < kFill; ++g) ask_rows(g, s1, within(128));
+#pragma unroll
+    for (int g = 0; g < kFill; ++g) ask_rows(g, s2, within(256));
+    arrive<2 * kFill>();
+    a[0] = decode_tile(0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) read(s0, i32 * 16 + place_of(i32, 4 * h), i, 0);
+    int kb = 0;
+    for (; kb + 512 <= K; kb += 512) {
+        multiply(s0, s1, s3, 0, kb);
+        multiply(s1, s2, s0, 1, kb + 128);
+        multiply(s2, s3, s1, 0, kb + 256);
+        multiply(s3, s0, s2, 1, kb + 384);
+    }
+    if (kb < K) multiply(s0, s1, s3, 0, kb);
+    if (kb + 128 < K) multiply(s1, s2, s0, 1, kb + 128);
+    if (kb + 256 < K) multiply(s2, s3, s1, 0, kb + 256);
+
+    // A lane holds outputs 8 p + 4 h .. + 3 (p = 0 .. 3) of token row i32 of
+    // each 32 x 32 tile.
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        const int m = i * 32 + i32;
+        if (m >= o.left) break;
+        uint16_t* row = y + (o.row0 + m) * N;
+#pragma unroll
+        for (int j = 0; j < (kSilu ? 1 : 2); ++j)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int n = o.n0 + wave * (kSilu ? 32 : 64) + j * 32 + 8 * p + 4 * h;
+                f32x4 v;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    v[c] = acc[i][j][4 * p + c];
+                    if (kSilu) v[c] = silu(v[c]) * acc[i][1][4 * p + c];
+                }
+                if (n < N) store4(row + n, v);
+            }
+    }
+}
+
+template <bool kSilu>
+__global__ __launch_bounds__(kTileThreads, 2) void tile_w4_kernel(
     const uint16_t* __restrict__ x, int64_t num_rows, const int32_t* __restrict__ expert_rows, int capacity,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N, int above,
     uint16_t* __restrict__ y) {
-    constexpr int kRows = 32 * kTiles, kOut = kSilu ? 128 : 256, kFill = 2 * kTiles;
-    __shared__ u32x4 even[kRows * 16], odd[kRows * 16];
+    constexpr int kOut = kSilu ? kTileWeights / 2 : kTileWeights;
+    __shared__ u32x4 s0[kTileRows * 16], s1[kTileRows * 16], s2[kTileRows * 16], s3[kTileRows * 16];
     extern __shared__ int32_t room[];
-    const int lane = lane_id(), h = lane / 32, i32 = lane % 32;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const Table t = make_table(room, expert_rows, E, capacity, num_rows, kRows, above, INT32_MAX);
+    const Table t = make_table(room, expert_rows, E, capacity, num_rows, kTileRows, above, INT32_MAX);
     const int columns = (N + kOut - 1) / kOut;
     const Share mine = share_of(static_cast<int64_t>(t.start[E]) * columns);
     for (int64_t item = mine.at; item < mine.end; item += mine.step) {
         const int tile = static_cast<int>(item / columns);
         const int e = expert_of(t, E, tile);
-        const int m0 = (tile - t.start[e]) * kRows;
+        const int m0 = (tile - t.start[e]) * kTileRows;
         const int left = __builtin_amdgcn_readfirstlane(t.count[e] - m0);
         const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
         const Operands o = operands<kSilu>(x, codes, scales, e, row0, left,
                                            static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut, K, N);
-        uint32_t cr[2], fill[kFill];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            cr[j] = code_offset(o, kSilu ? wave * 32 + i32 : wave * 64 + j * 32 + i32, N, K, h);
-        // This wave fills rows 8 kTiles wave .. on, four to a load: lane l writes
-        // place l % 16 of row l / 16, so it reads the inputs that belong there.
-#pragma unroll
-        for (int i = 0; i < kFill; ++i) {
-            const int r = wave * 8 * kTiles + i * 4 + lane / 16;
-            fill[i] = __umul24(r < left ? r : left - 1, K * 2) + place_of(r, lane % 16) * 16;
-        }
-        auto stage = [&](u32x4* to, int kb) {
-#pragma unroll
-            for (int i = 0; i < kFill; ++i)
-                load_shared(to + (wave * 8 * kTiles + i * 4) * 16, o.xb, fill[i], kb * 2);
-        };
-        u32x4 w[2][2][2];                           // [buffer][weight tile][u]
-        uint32_t b[2][2];                           // the four scales of 128 inputs
-        auto load = [&](int buf, int kb) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                w[buf][j][0] = load16(o.wb[kSilu ? j : 0], cr[j], kb / 2);
-                w[buf][j][1] = load16(o.wb[kSilu ? j : 0], cr[j], kb / 2 + 32);
-                b[buf][j] = load4(o.sb[kSilu ? j : 0], cr[j] / 16 - h, kb / 32);
-            }
-        };
-        f32x16 acc[kTiles][2] = {};
-        auto multiply = [&](const u32x4* from, int buf) {
-            bf16x8 v[kTiles], a[2];
-            // Place 4 h of row i32, from which the others differ by an exclusive or:
-            // worked out anew from one register, which the compiler may not see
-            // through, or it keeps one for every place.
-            int first = i32 * 16 + place_of(i32, 4 * h);
-            asm("" : "+v"(first));
-            auto read = [&](int i, int us) {
-                v[i] = __builtin_bit_cast(bf16x8, from[i * 512 + (first ^ ((us & 4) * 2 + us % 4))]);
-            };
-            auto decode_tile = [&](int j, int us) {
-                const uint32_t scale = (b[buf][j] >> (8 * h + 16 * (us / 4)) & 0xFF) << 23;
-                return decode(w[buf][j][us / 4][us % 4], __uint_as_float(scale));
-            };
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) read(i, 0);
-            a[0] = decode_tile(0, 0);
-            // Each weight tile is decoded beside the products of the one before,
-            // and the next inputs of a row tile read when its last product is
-            // under way.  The barriers to scheduling keep it that way: left
-            // alone, all reads and decodes move to the front and spill.
-#pragma unroll
-            for (int us = 0; us < 8; ++us)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (j == 0) a[1] = decode_tile(1, us);
-                    else if (us < 7) a[0] = decode_tile(0, us + 1);
-#pragma unroll
-                    for (int i = 0; i < kTiles; ++i) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[j], v[i], acc[i][j], 0, 0, 0);
-                        if (j == 1 && us < 7) {
-                            read(i, us + 1);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                    }
-                }
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        // A step's loads have arrived (vmcnt), in every wave (barrier), and every
-        // wave is done with the step before, whose buffer the next loads fill.
-        auto arrive = [&] {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-        };
-        // No branch in the loop: past the end the last step is asked for again.
-        __syncthreads();                            // the last item's reads are done
-        stage(even, 0);
-        load(0, 0);
-        int kb = 0;
-        for (; kb + 256 <= K; kb += 256) {
-            arrive();
-            stage(odd, kb + 128);
-            load(1, kb + 128);
-            multiply(even, 0);
-            arrive();
-            const int next = kb + 256 < K ? kb + 256 : K - 128;
-            stage(even, next);
-            load(0, next);
-            multiply(odd, 1);
-        }
-        if (kb < K) {
-            arrive();
-            multiply(even, 0);
-        }
-
-        // A lane holds outputs 8 p + 4 h .. + 3 (p = 0 .. 3) of token row i32 of
-        // each 32 x 32 tile.
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            const int m = i * 32 + i32;
-            if (m >= left) break;
-            uint16_t* row = y + (row0 + m) * N;
-#pragma unroll
-            for (int j = 0; j < (kSilu ? 1 : 2); ++j)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int n = o.n0 + wave * (kSilu ? 32 : 64) + j * 32 + 8 * p + 4 * h;
-                    f32x4 v;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        v[c] = acc[i][j][4 * p + c];
-                        if (kSilu) v[c] = silu(v[c]) * acc[i][1][4 * p + c];
-                    }
-                    if (n < N) store4(row + n, v);
-                }
-        }
+        // An expert's last tile is not full: products of rows that are not there
+        // would cost what the others do.
+        if (left > 96) tile_item<kSilu, 4>(o, K, N, y, s0, s1, s2, s3);
+        else if (left > 64) tile_item<kSilu, 3>(o, K, N, y, s0, s1, s2, s3);
+        else if (left > 32) tile_item<kSilu, 2>(o, K, N, y, s0, s1, s2, s3);
+        else tile_item<kSilu, 1>(o, K, N, y, s0, s1, s2, s3);
     }
 }
 
@@ -553,16 +582,15 @@ hipError_t launch_stream(const Call& c, int most) {
     return c.K % 256 == 0 ? launch_stream<kSilu, true>(c, most) : launch_stream<kSilu, false>(c, most);
 }
 
-template <bool kSilu, int kTiles>
+template <bool kSilu>
 hipError_t launch_tile(const Call& c, int above) {
-    const int64_t items = most_tiles(c, 32 * kTiles) * ceil_div(c.N, kSilu ? 128 : 256);
-    hipLaunchKernelGGL((tile_w4_kernel<kSilu, kTiles>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads),
-                       table_bytes(c.E), c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows,
-                       c.capacity, c.codes, c.scales, c.E, c.K, c.N, above, static_cast<uint16_t*>(c.y));
+    const int64_t items = most_tiles(c, kTileRows) * ceil_div(c.N, kSilu ? kTileWeights / 2 : kTileWeights);
+    hipLaunchKernelGGL((tile_w4_kernel<kSilu>), dim3(blocks_for(items, 256)), dim3(kTileThreads), table_bytes(c.E),
+                       c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows, c.capacity, c.codes,
+                       c.scales, c.E, c.K, c.N, above, static_cast<uint16_t*>(c.y));
     return hipGetLastError();
 }
 
-constexpr int kSmallTile = 96;
 constexpr int kFew = 32;    // rows of an expert up to which its weights are streamed
 
 template <bool kSilu>
@@ -570,11 +598,11 @@ hipError_t launch(const Call& c) {
     // What an expert holds at most (a packed batch: on average).
     const int64_t rows = c.capacity > 0 ? c.capacity : c.num_rows / c.E;
     if (rows <= kFew) return launch_stream<kSilu>(c, INT32_MAX);
-    if (c.capacity == 0) return rows <= kSmallTile ? launch_tile<kSilu, 2>(c, 0) : launch_tile<kSilu, 4>(c, 0);
+    if (c.capacity == 0) return launch_tile<kSilu>(c, 0);
     // A padded region says little about how many of its rows are filled: each
     // launch takes the experts that suit it.
     const hipError_t e = launch_stream<kSilu>(c, kFew);
-    return e != hipSuccess ? e : launch_tile<kSilu, 4>(c, kFew);
+    return e != hipSuccess ? e : launch_tile<kSilu>(c, kFew);
 }
 
 }  // namespace
