@@ -201,7 +201,7 @@ __device__ __forceinline__ uint32_t code_offset(const Operands& o, int n, int N,
 
 // ---- few rows per expert: bound by reading the weights ---------------------------
 // A wave takes 64 weight rows (kSilu: 32 gate rows and their 32 up rows) and up
-// to 32 token rows, 256 inputs at a time: whole 128-byte lines of the codes (64
+// to 16 token rows, 256 inputs at a time: whole 128-byte lines of the codes (64
 // bytes of twice as many rows is a fifth slower from HBM) and, kEven, their eight
 // scales in one load (byte loads cost a quarter of the whole).  Where there are
 // items for every wave, each takes whole items; where there are not (a single
@@ -210,20 +210,31 @@ __device__ __forceinline__ uint32_t code_offset(const Operands& o, int n, int N,
 // order.  Nothing is staged: the four waves of a block read the same token rows,
 // which the L1 holds, and never wait for each other.
 
-// acc += the products of kTiles row tiles over inputs k, k + step, ...
-// kEven: K % 256 == 0.
-template <bool kSilu, bool kEven, int kTiles>
+// Register s of the lanes of group q (lane / 16) and register q of group s change
+// places: halves of the wave first, then neighbouring groups.
+__device__ __forceinline__ void transpose_groups(u32x4 (&v)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const u32x2 a = __builtin_amdgcn_permlane32_swap(v[0][c], v[2][c], false, false);
+        const u32x2 b = __builtin_amdgcn_permlane32_swap(v[1][c], v[3][c], false, false);
+        const u32x2 even = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+        const u32x2 odd = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+        v[0][c] = even[0];
+        v[1][c] = even[1];
+        v[2][c] = odd[0];
+        v[3][c] = odd[1];
+    }
+}
+
+// acc += the products over inputs k, k + step, ...  kEven: K % 256 == 0.
+template <bool kSilu, bool kEven>
 __device__ __forceinline__ void stream_products(const Operands& o, int k, int step, int K, int N, int q, int i16,
-                                                f32x4 (*acc)[4]) {
-    uint32_t cr[4], xr[kTiles];
+                                                f32x4* acc) {
+    uint32_t cr[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) cr[j] = code_offset(o, (kSilu ? j % 2 : j) * 16 + i16, N, K, q);
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-        const int m = i * 16 + i16 < o.left ? i * 16 + i16 : o.left - 1;
-        xr[i] = __umul24(m, K * 2) + q * 64;
-    }
-    u32x4 w[2][2][4], v[2][kTiles][4];              // [buffer][half][weight tile], [half][row tile][..]
+    const uint32_t xr = __umul24(i16 < o.left ? i16 : o.left - 1, K * 2) + q * 16;
+    u32x4 w[2][2][4], v[2][4];                      // [buffer][half][weight tile], [half][..]
     u32x2 b[2][4];
     // Every load below is made on every way through the loop, past the end
     // again from the last block: a branch around a load makes the compiler wait
@@ -246,14 +257,16 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
             }
         }
     };
+    // Load s brings group q inputs 32 s + 8 q .. + 7: 64 bytes in a row of each
+    // token row (the inputs 32 q + 8 s .. that step s needs lie 64 bytes apart, and
+    // four times the cache lookups made these loads cost what the weights do).
     auto rows = [&](int h, int at) {
         at = at < K ? at : K - 128;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) v[h][i][s] = load16(o.xb, xr[i], (at + 8 * s) * 2);
+        for (int s = 0; s < 4; ++s) v[h][s] = load16(o.xb, xr, (at + 32 * s) * 2);
     };
     auto multiply = [&](int buf, int h) {
+        transpose_groups(v[h]);
         float scale[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -261,13 +274,9 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bf16x8 a = decode(w[buf][h][j][s], scale[j]);
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, v[h][i][s]),
-                                                                        acc[i][j], 0, 0, 0);
-            }
+            for (int j = 0; j < 4; ++j)
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode(w[buf][h][j][s], scale[j]),
+                                                                 __builtin_bit_cast(bf16x8, v[h][s]), acc[j], 0, 0, 0);
     };
     // Loads return in order: token rows are asked for before the weights that may
     // stay on the way while they are waited for.
@@ -292,7 +301,7 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
 }
 
 template <bool kSilu, bool kEven>
-__global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
+__global__ __launch_bounds__(kThreads, 3) void stream_w4_kernel(
     const uint16_t* __restrict__ x, int64_t num_rows, const int32_t* __restrict__ expert_rows, int capacity,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N, int most,
     uint16_t* __restrict__ y) {
@@ -301,7 +310,7 @@ __global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
     extern __shared__ int32_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const Table t = make_table(room, expert_rows, E, capacity, num_rows, 32, 0, most);
+    const Table t = make_table(room, expert_rows, E, capacity, num_rows, 16, 0, most);
     const int columns = (N + kOut - 1) / kOut;
     const int64_t items = static_cast<int64_t>(t.start[E]) * columns;
     const bool split = items < kSplitBelow * static_cast<int64_t>(gridDim.x);
@@ -314,51 +323,45 @@ __global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
         const int tile = static_cast<int>(item / columns);
         const int column = static_cast<int>(item - static_cast<int64_t>(tile) * columns);
         const int e = expert_of(t, E, tile);
-        const int m0 = (tile - t.start[e]) * 32;
+        const int m0 = (tile - t.start[e]) * 16;
         const int left = __builtin_amdgcn_readfirstlane(t.count[e] - m0);
         const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
         const Operands o = operands<kSilu>(x, codes, scales, e, row0, left, column * kOut, K, N);
-        f32x4 acc[2][4] = {};
-        const int k = split ? wave * 256 : 0, step = split ? 1024 : 256;
-        if (left <= 16) stream_products<kSilu, kEven, 1>(o, k, step, K, N, q, i16, acc);
-        else stream_products<kSilu, kEven, 2>(o, k, step, K, N, q, i16, acc);
+        f32x4 acc[4] = {};
+        stream_products<kSilu, kEven>(o, split ? wave * 256 : 0, split ? 1024 : 256, K, N, q, i16, acc);
 
+        // A lane holds outputs 4 q .. + 3 of token row i16 of each 16 x 16 tile; of
+        // split items wave w ends up with weight tile w (kSilu: waves 0 and 1
+        // with the gate's and the up rows').
+        uint16_t* row = y + (row0 + i16) * N;
+        if (split) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i * 16 >= left) break;
-            // A lane holds outputs 4 q .. + 3 of token row i16 of each 16 x 16
-            // tile; of split items wave w ends up with weight tile w (kSilu: waves
-            // 0 and 1 with the gate's and the up rows').
-            const int m = i * 16 + i16;
-            if (split) {
+            for (int j = 0; j < 4; ++j) part[wave][j][lane] = acc[j];
+            __syncthreads();
+            auto sum = [&](int j) {
+                return (part[0][j][lane] + part[1][j][lane]) + (part[2][j][lane] + part[3][j][lane]);
+            };
+            const int n = o.n0 + wave * 16 + 4 * q;
+            if (wave * 16 < kOut && i16 < left && n < N) {
+                f32x4 u = sum(wave);
+                if (kSilu) {
+                    const f32x4 up = sum(wave + 2);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) part[wave][j][lane] = acc[i][j];
-                __syncthreads();
-                auto sum = [&](int j) {
-                    return (part[0][j][lane] + part[1][j][lane]) + (part[2][j][lane] + part[3][j][lane]);
-                };
-                const int n = o.n0 + wave * 16 + 4 * q;
-                if (wave * 16 < kOut && m < left && n < N) {
-                    f32x4 u = sum(wave);
-                    if (kSilu) {
-                        const f32x4 up = sum(wave + 2);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) u[c] = silu(u[c]) * up[c];
-                    }
-                    store4(y + (row0 + m) * N + n, u);
+                    for (int c = 0; c < 4; ++c) u[c] = silu(u[c]) * up[c];
                 }
-                __syncthreads();
-            } else if (m < left) {
+                store4(row + n, u);
+            }
+            __syncthreads();
+        } else if (i16 < left) {
 #pragma unroll
-                for (int j = 0; j < kOut / 16; ++j) {
-                    const int n = o.n0 + j * 16 + 4 * q;
-                    f32x4 u = acc[i][j];
-                    if (kSilu) {
+            for (int j = 0; j < kOut / 16; ++j) {
+                const int n = o.n0 + j * 16 + 4 * q;
+                f32x4 u = acc[j];
+                if (kSilu) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) u[c] = silu(u[c]) * acc[i][j + 2][c];
-                    }
-                    if (n < N) store4(y + (row0 + m) * N + n, u);
+                    for (int c = 0; c < 4; ++c) u[c] = silu(u[c]) * acc[j + 2][c];
                 }
+                if (n < N) store4(row + n, u);
             }
         }
     }
@@ -571,8 +574,8 @@ int64_t most_tiles(const Call& c, int rows) { return c.num_rows / rows + (c.num_
 
 template <bool kSilu, bool kEven>
 hipError_t launch_stream(const Call& c, int most) {
-    const int64_t items = most_tiles(c, 32) * ceil_div(c.N, kSilu ? 32 : 64);
-    hipLaunchKernelGGL((stream_w4_kernel<kSilu, kEven>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads),
+    const int64_t items = most_tiles(c, 16) * ceil_div(c.N, kSilu ? 32 : 64);
+    hipLaunchKernelGGL((stream_w4_kernel<kSilu, kEven>), dim3(blocks_for(items, 256 * 3)), dim3(kThreads),
                        table_bytes(c.E), c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows,
                        c.capacity, c.codes, c.scales, c.E, c.K, c.N, most, static_cast<uint16_t*>(c.y));
     return hipGetLastError();
@@ -591,18 +594,19 @@ hipError_t launch_tile(const Call& c, int above) {
     return hipGetLastError();
 }
 
-constexpr int kFew = 32;    // rows of an expert up to which its weights are streamed
+constexpr int kFew = 16;    // rows of an expert up to which its weights are streamed
 
 template <bool kSilu>
 hipError_t launch(const Call& c) {
-    // What an expert holds at most (a packed batch: on average).
-    const int64_t rows = c.capacity > 0 ? c.capacity : c.num_rows / c.E;
-    if (rows <= kFew) return launch_stream<kSilu>(c, INT32_MAX);
-    if (c.capacity == 0) return launch_tile<kSilu>(c, 0);
-    // A padded region says little about how many of its rows are filled: each
-    // launch takes the experts that suit it.
-    const hipError_t e = launch_stream<kSilu>(c, kFew);
-    return e != hipSuccess ? e : launch_tile<kSilu>(c, kFew);
+    // The rows of an expert are known on the device only; each launch takes the
+    // experts that suit it, and one is left out where it would find none or few.
+    const int64_t most = c.capacity > 0 ? c.capacity : c.num_rows, mean = c.num_rows / c.E;
+    if (c.capacity > 0 || mean <= 2 * kFew) {
+        const hipError_t e = launch_stream<kSilu>(c, kFew);
+        if (e != hipSuccess || most <= kFew) return e;
+        return launch_tile<kSilu>(c, kFew);
+    }
+    return launch_tile<kSilu>(c, 0);
 }
 
 }  // namespace
