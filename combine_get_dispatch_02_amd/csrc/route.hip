@@ -1,8 +1,16 @@
 // route.hip -- ep_route and ep_route_backward on gfx950.
 //
 // Router logits [T, E] to the k experts of each token and their weights, and
-// the gradient back.  L lanes of a wave hold one token (64 / L tokens per
-// wave), C of its experts each: expert e = c * L + lane.
+// the gradient back.
+//
+// Choosing.  L lanes of a wave hold one token (64 / L tokens a wave), C of its
+// experts each, in order: lane p has experts C p .. C p + C - 1.  A choice and its
+// expert make one 64-bit key that is also a positive double, so that one
+// instruction (v_max_f64, as fast as an fp32 one here) compares both, ties
+// included.  Every lane sorts its keys once (a network of v_max / v_min); each of
+// the k rounds is then a maximum over the lanes' first keys, and the lane that
+// had it moves up its list.  For 32768 tokens of 256 experts, top 8, that is
+// about 80 instructions a token where repeated scans took 600.
 #include "../../include/ep.h"
 #include "ep_device.h"
 #include "ep_launch.h"
@@ -32,17 +40,59 @@ __device__ __forceinline__ float logit(const typename In::raw* p) {
     return v != v ? -kInf : v;
 }
 
+// ---- one token's lanes -----------------------------------------------------------
+// v combined over the L lanes of a token, in every lane: by rotations within the
+// rows of 16 lanes, then by exchanging rows and halves.
+template <int kRotate>
+__device__ __forceinline__ uint32_t rotate_row(uint32_t v) {
+    return __builtin_amdgcn_update_dpp(0, v, 0x120 + kRotate, 0xF, 0xF, true);  // row_ror
+}
+template <int kRotate>
+__device__ __forceinline__ float rotate_row(float v) {
+    return __uint_as_float(rotate_row<kRotate>(__float_as_uint(v)));
+}
+template <int kRotate>
+__device__ __forceinline__ double rotate_row(double v) {
+    const u32x2 u = __builtin_bit_cast(u32x2, v);
+    return __builtin_bit_cast(double, u32x2{rotate_row<kRotate>(u[0]), rotate_row<kRotate>(u[1])});
+}
+// The two values that neighbouring rows (kHalf: the halves of the wave) hold.
+template <bool kHalf>
+__device__ __forceinline__ u32x2 exchange(uint32_t v) {
+    return kHalf ? __builtin_amdgcn_permlane32_swap(v, v, false, false)
+                 : __builtin_amdgcn_permlane16_swap(v, v, false, false);
+}
+template <bool kHalf, typename Op>
+__device__ __forceinline__ float exchange(float v, Op op) {
+    const u32x2 u = exchange<kHalf>(__float_as_uint(v));
+    return op(__uint_as_float(u[0]), __uint_as_float(u[1]));
+}
+template <bool kHalf, typename Op>
+__device__ __forceinline__ double exchange(double v, Op op) {
+    const u32x2 u = __builtin_bit_cast(u32x2, v);
+    const u32x2 lo = exchange<kHalf>(u[0]), hi = exchange<kHalf>(u[1]);
+    return op(__builtin_bit_cast(double, u32x2{lo[0], hi[0]}), __builtin_bit_cast(double, u32x2{lo[1], hi[1]}));
+}
+template <int L, typename F, typename Op>
+__device__ __forceinline__ F over_lanes(F v, Op op) {
+    static_assert(L == 16 || L == 64, "a row of lanes or the whole wave");
+    v = op(v, rotate_row<8>(v));
+    v = op(v, rotate_row<4>(v));
+    v = op(v, rotate_row<2>(v));
+    v = op(v, rotate_row<1>(v));
+    if (L == 64) {
+        v = exchange<false>(v, op);
+        v = exchange<true>(v, op);
+    }
+    return v;
+}
 template <int L>
 __device__ __forceinline__ float max_over(float v) {
-#pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return over_lanes<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 template <int L, typename F>
 __device__ __forceinline__ F sum_over(F v) {
-#pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+    return over_lanes<L>(v, [](F a, F b) { return a + b; });
 }
 
 // exp(l - top) as a softmax term: 0 for an unavailable expert, and 1 for each
@@ -51,9 +101,37 @@ __device__ __forceinline__ float softmax_term(float l, float top) {
     if (l == top) return l == -kInf ? 0.0f : 1.0f;
     return expf(l - top);
 }
+
+// exp(x) to about 2^-50 for |x| <= 700: x = n ln 2 + r with |r| <= ln 2 / 2, the
+// Taylor series of exp(r) to r^12 (the next term is below 2^-52), scaled by 2^n.
+__device__ __forceinline__ double exp64(double x) {
+    const double n = __builtin_rint(x * 1.4426950408889634074);
+    double r = __builtin_fma(n, -0.6931471805437468, x);    // ln 2 = its first 34 bits,
+    r = __builtin_fma(n, -1.619851018665656e-11, r);        // exact times n, and the rest
+    double p = 1.0 / 479001600;
+    p = __builtin_fma(p, r, 1.0 / 39916800);
+    p = __builtin_fma(p, r, 1.0 / 3628800);
+    p = __builtin_fma(p, r, 1.0 / 362880);
+    p = __builtin_fma(p, r, 1.0 / 40320);
+    p = __builtin_fma(p, r, 1.0 / 5040);
+    p = __builtin_fma(p, r, 1.0 / 720);
+    p = __builtin_fma(p, r, 1.0 / 120);
+    p = __builtin_fma(p, r, 1.0 / 24);
+    p = __builtin_fma(p, r, 1.0 / 6);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
+}
+// 1 / d for d in [1, 2^1000]: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double reciprocal64(double d) {
+    double r = __builtin_amdgcn_rcp(d);
+    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
 __device__ __forceinline__ double softmax_term64(float l, float top) {
     if (l == top) return l == -kInf ? 0.0 : 1.0;
-    return exp(static_cast<double>(l) - static_cast<double>(top));
+    return exp64(fmax(static_cast<double>(l) - static_cast<double>(top), -700.0));
 }
 
 // sigmoid(l) * exp(-low), low = min(0, largest chosen logit): numerator and
@@ -64,145 +142,226 @@ __device__ __forceinline__ float sigmoid_over(float l, float low) {
 }
 __device__ __forceinline__ float sigmoid(float l) { return sigmoid_over(l, 0.0f); }
 __device__ __forceinline__ double sigmoid64(float l) {
-    return 1.0 / (1.0 + exp(-static_cast<double>(l)));
+    return reciprocal64(1.0 + exp64(fmin(fmax(-static_cast<double>(l), -700.0), 700.0)));
 }
 
-// Choice and expert in one 64-bit key: larger choices first, and of equal
-// choices the lower expert.  0: unavailable.  -0 counts as 0.
-__device__ __forceinline__ uint64_t make_key(float choice, int e) {
-    if (!(choice > -kInf)) return 0;
+// ---- keys ------------------------------------------------------------------------
+// Choice and expert in one double: 1 + a fraction of 32 bits that order the choice
+// and 16 that order equal choices, the lower expert first.  1: unavailable.  -0
+// counts as 0.
+constexpr uint64_t kNoKey = 0x3FF0000000000000ull;
+__device__ __forceinline__ double make_key(float choice, int e) {
     const uint32_t u = __float_as_uint(choice + 0.0f);
-    const uint32_t ordered = u & 0x80000000u ? ~u : u | 0x80000000u;
-    return static_cast<uint64_t>(ordered) << 16 | static_cast<uint64_t>(0xFFFF - e);
+    const uint32_t ordered = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+    const uint64_t key = kNoKey | static_cast<uint64_t>(ordered) << 16 | static_cast<uint64_t>(0xFFFF - e);
+    return __builtin_bit_cast(double, choice > -kInf ? key : kNoKey);
 }
-__device__ __forceinline__ int key_expert(uint64_t key) { return 0xFFFF - static_cast<int>(key & 0xFFFF); }
+__device__ __forceinline__ bool is_key(double key) { return __builtin_bit_cast(uint64_t, key) != kNoKey; }
+__device__ __forceinline__ int key_expert(double key) {
+    return 0xFFFF - static_cast<int>(__builtin_bit_cast(uint64_t, key) & 0xFFFF);
+}
+__device__ __forceinline__ float key_choice(double key) {
+    const uint32_t ordered = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, key) >> 16);
+    return __uint_as_float(ordered & 0x80000000u ? ordered ^ 0x80000000u : ~ordered);
+}
+// (As the builtins these are preceded by one instruction an operand that quiets
+// NaNs, which keys never are.)
+__device__ __forceinline__ double key_max(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ double key_min(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
 
-template <int L>
-__device__ __forceinline__ uint64_t max_key_over(uint64_t v) {
+// Largest first: Batcher's odd-even merge sort.
+template <int C>
+__device__ __forceinline__ void sort_keys(double (&k)[C]) {
 #pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) {
-        const uint64_t o = static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(v), d));
-        v = o > v ? o : v;
-    }
-    return v;
+    for (int p = 1; p < C; p *= 2)
+#pragma unroll
+        for (int d = p; d > 0; d /= 2)
+#pragma unroll
+            for (int i = 0; i < C - d; ++i)
+                if (i >= d % p && (i - d % p) / d % 2 == 0 && i / (2 * p) == (i + d) / (2 * p)) {
+                    const double a = key_max(k[i], k[i + d]), b = key_min(k[i], k[i + d]);
+                    k[i] = a;
+                    k[i + d] = b;
+                }
 }
 
-template <typename In, int L, int C>
+// The C logits from p on, of which the first n exist, and -inf for the others.
+template <typename In, int C>
+__device__ __forceinline__ void load_logits(const typename In::raw* p, int n, float (&l)[C]) {
+    // (Elements may lie anywhere: global loads need no alignment.)
+    typedef typename In::raw Vector __attribute__((ext_vector_type(C), aligned(sizeof(typename In::raw))));
+    if (n >= C) {
+        const Vector v = *reinterpret_cast<const Vector*>(p);
+#pragma unroll
+        for (int c = 0; c < C; ++c) l[c] = to_float(In(), v[c]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) l[c] = c < n ? to_float(In(), p[c]) : -kInf;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (l[c] != l[c]) l[c] = -kInf;
+}
+
+// Whether the calling lane's experts are in a kept group, where every group is a
+// power of two of whole lanes: kept[c] for each.
+struct Best {
+    float first, second;                            // -inf: none
+};
+__device__ __forceinline__ Best best_of(Best a, Best b) {
+    return {fmaxf(a.first, b.first), fmaxf(fminf(a.first, b.first), fmaxf(a.second, b.second))};
+}
+// A group's score; of the two best the second counts only if there is one.
+__device__ __forceinline__ float group_score(Best b, int group_top) {
+    return group_top == 2 && b.second > -kInf ? b.first + b.second : b.first;
+}
+
+// D: how far down a lane's list k rounds can get, min(C, k) or more.
+template <typename In, int L, int C, int D>
 __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In::raw* __restrict__ logits,
                                                               const float* __restrict__ bias, int64_t T,
                                                               int E, int k, RouteOptions opt,
                                                               int64_t* __restrict__ topk_idx,
                                                               float* __restrict__ topk_weights) {
     constexpr int kTokens = kWave / L;
-    extern __shared__ float choices[];              // [kWaves * kTokens][E], groups only
+    extern __shared__ float choices[];              // [kWaves * kTokens][E], groups of other sizes only
     const int lane = lane_id(), pos = lane % L, sub = lane / L;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const bool by_choice = bias || (opt.num_groups > 1 && opt.group_top == 2);
+    const int e0 = pos * C, size = E / opt.num_groups;
+    float b[C] = {};
+    if (bias) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (e0 + c < E) b[c] = bias[e0 + c];
+    }
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kTokens;
     for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTokens; t0 < T; t0 += step) {
         const bool live = t0 + sub < T;
         const int64_t t = live ? t0 + sub : T - 1;  // lanes past the end repeat the last token
         float l[C];
+        load_logits<In, C>(logits + t * E + e0, E - e0, l);
         float top = -kInf;
+        if (!opt.sigmoid) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int e = c * L + pos;
-            l[c] = e < E ? logit<In>(logits + t * E + e) : -kInf;
-            top = fmaxf(top, l[c]);
+            for (int c = 0; c < C; ++c) top = fmaxf(top, l[c]);
+            top = max_over<L>(top);
         }
-        top = max_over<L>(top);
 
         float choice[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) choice[c] = l[c];
         if (by_choice) {
-            double total = 1.0;
-            if (!opt.sigmoid) {
-                total = 0.0;
+            // fl32 of the 64-bit score: an fp32 one is off by a step or two, enough
+            // to put neighbours in another order.
+            if (opt.sigmoid) {
 #pragma unroll
-                for (int c = 0; c < C; ++c) total += softmax_term64(l[c], top);
+                for (int c = 0; c < C; ++c) choice[c] = static_cast<float>(sigmoid64(l[c]));
+            } else {
+                double s[C], total = 0.0;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    s[c] = softmax_term64(l[c], top);
+                    total += s[c];
+                }
                 total = sum_over<L>(total);
+                const double inverse = reciprocal64(total);     // total >= 1, or none is available
+#pragma unroll
+                for (int c = 0; c < C; ++c) choice[c] = static_cast<float>(s[c] * inverse);
             }
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int e = c * L + pos;
-                const double s = opt.sigmoid ? sigmoid64(l[c]) : softmax_term64(l[c], top) / total;
-                const float b = bias && e < E ? bias[e] : 0.0f;
-                choice[c] = l[c] > -kInf ? static_cast<float>(s) + b : -kInf;
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; ++c) choice[c] = l[c];
+            for (int c = 0; c < C; ++c) choice[c] = l[c] > -kInf ? choice[c] + b[c] : -kInf;
         }
 
-        uint64_t kept = ~uint64_t(0);
         if (opt.num_groups > 1) {
-            float* row = choices + (wave * kTokens + sub) * E;
-            const int size = E / opt.num_groups;
+            const int wide = size / C;              // lanes of a group, if whole and a power of two
+            if (E == L * C && wide * C == size && (wide & (wide - 1)) == 0) {
+                Best best = {-kInf, -kInf};
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (c * L + pos < E) row[c * L + pos] = choice[c];
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            // Every lane scores the groups g = pos, pos + L, ...; of two NaN-free
-            // bests the second counts only if it is available.
-            float* score = row;                     // overwritten below, group by group
-            kept = 0;
-            float mine[kWave / L];
-#pragma unroll
-            for (int i = 0; i < kWave / L; ++i) {
-                const int g = i * L + pos;
-                float first = -kInf, second = -kInf;
-                if (g < opt.num_groups)
-                    for (int u = 0; u < size; ++u) {
-                        const float v = row[g * size + u];
-                        if (v > first) {
-                            second = first;
-                            first = v;
-                        } else if (v > second) {
-                            second = v;
-                        }
-                    }
-                mine[i] = first;
-                if (opt.group_top == 2 && second > -kInf) mine[i] = first + second;
-            }
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int i = 0; i < kWave / L; ++i)
-                if (i * L + pos < opt.num_groups) score[i * L + pos] = mine[i];
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            for (int g = 0; g < opt.num_groups; ++g) {
-                const float v = score[g];
+                for (int c = 0; c < C; ++c) best = best_of(best, {choice[c] == choice[c] ? choice[c] : -kInf, -kInf});
+                for (int d = 1; d < wide; d *= 2)
+                    best = best_of(best, {__shfl_xor(best.first, d), __shfl_xor(best.second, d)});
+                const float mine = group_score(best, opt.group_top);
+                const int first = pos & ~(wide - 1);
                 int better = 0;
-                for (int o = 0; o < opt.num_groups; ++o)
-                    better += score[o] > v || (score[o] == v && o < g);
-                if (better < opt.topk_groups) kept |= uint64_t(1) << g;
+                for (int o = 0; o < L; o += wide) {
+                    const float v = __shfl(mine, sub * L + o);
+                    better += v > mine || (v == mine && o < first);
+                }
+                if (better >= opt.topk_groups) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) choice[c] = -kInf;
+                }
+            } else {
+                // Any size: through shared memory, a lane to a group.
+                float* row = choices + (wave * kTokens + sub) * E;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (e0 + c < E) row[e0 + c] = choice[c];
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                float mine[kWave / L];
+#pragma unroll
+                for (int i = 0; i < kWave / L; ++i) {
+                    const int g = i * L + pos;
+                    Best best = {-kInf, -kInf};
+                    if (g < opt.num_groups)
+                        for (int u = 0; u < size; ++u) {
+                            const float v = row[g * size + u];
+                            best = best_of(best, {v == v ? v : -kInf, -kInf});
+                        }
+                    mine[i] = group_score(best, opt.group_top);
+                }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int i = 0; i < kWave / L; ++i)
+                    if (i * L + pos < opt.num_groups) row[i * L + pos] = mine[i];
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                uint64_t kept = 0;
+                for (int g = 0; g < opt.num_groups; ++g) {
+                    const float v = row[g];
+                    int better = 0;
+                    for (int o = 0; o < opt.num_groups; ++o) better += row[o] > v || (row[o] == v && o < g);
+                    if (better < opt.topk_groups) kept |= uint64_t(1) << g;
+                }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (e0 + c < E && !(kept >> ((e0 + c) / size) & 1)) choice[c] = -kInf;
             }
-            __builtin_amdgcn_wave_barrier();
         }
 
-        uint64_t key[C];
-        const int size = E / opt.num_groups;
+        double key[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int e = c * L + pos;
-            key[c] = e < E && (kept >> (e / size) & 1) ? make_key(choice[c], e) : 0;
-        }
-        // k rounds: the largest key of the token's lanes goes to lane j.
-        uint64_t won = 0;
+        for (int c = 0; c < C; ++c) key[c] = make_key(choice[c], e0 + c);
+        sort_keys<C>(key);
+        // k rounds: the largest first key of the token's lanes goes to lane j, and
+        // the lane that had it moves up.
+        double won = __builtin_bit_cast(double, kNoKey);
         for (int j = 0; j < k; ++j) {
-            uint64_t best = 0;
-#pragma unroll
-            for (int c = 0; c < C; ++c) best = key[c] > best ? key[c] : best;
-            best = max_key_over<L>(best);
+            const double best = over_lanes<L>(key[0], [](double x, double y) { return key_max(x, y); });
             if (pos == j) won = best;
+            const bool had = key[0] == best;
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (key[c] == best) key[c] = 0;
+            for (int i = 0; i < D; ++i) {
+                const double next = i + 1 < C ? key[i + 1] : __builtin_bit_cast(double, kNoKey);
+                key[i] = had ? next : key[i];
+            }
         }
 
-        const bool filled = pos < k && won != 0;
+        const bool filled = pos < k && is_key(won);
         const int e = filled ? key_expert(won) : -1;
-        const float le = filled ? logit<In>(logits + t * E + e) : -kInf;
+        float le = -kInf;
+        if (filled) le = by_choice ? logit<In>(logits + t * E + e) : key_choice(won);
         float a, total = 1.0f;
         if (opt.sigmoid) {
             const float low = opt.renormalize ? fminf(max_over<L>(le), 0.0f) : 0.0f;
@@ -211,9 +370,13 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In:
             const float m = opt.renormalize ? max_over<L>(le) : top;
             a = softmax_term(le, m);
             if (!opt.renormalize) {
+                // 2^x of the hardware: off by a step and by 2.5 units of l - top,
+                // which is small where a term counts.
                 total = 0.0f;
 #pragma unroll
-                for (int c = 0; c < C; ++c) total += softmax_term(l[c], top);
+                for (int c = 0; c < C; ++c)
+                    total += l[c] == top ? (top > -kInf ? 1.0f : 0.0f)
+                                         : __builtin_amdgcn_exp2f((l[c] - top) * 1.44269504f);
                 total = sum_over<L>(total);
             }
         }
@@ -294,25 +457,37 @@ __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(
     }
 }
 
-template <typename In, int L, int C>
-hipError_t launch_lc(const void* logits, const float* bias, int64_t T, int E, int k, const RouteOptions& opt,
-                     int64_t* topk_idx, float* topk_weights, hipStream_t stream) {
+template <typename In, int L, int C, int D>
+hipError_t launch_lanes(const void* logits, const float* bias, int64_t T, int E, int k, const RouteOptions& opt,
+                        int64_t* topk_idx, float* topk_weights, hipStream_t stream) {
     const int per_block = kWaves * (kWave / L);
     const int64_t blocks = ceil_div(T, per_block), cap = kMaxLaunchThreads / (kWaves * kWave);
     const size_t lds = opt.num_groups > 1 ? sizeof(float) * per_block * E : 0;
-    hipLaunchKernelGGL((route_kernel<In, L, C>), dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
+    hipLaunchKernelGGL((route_kernel<In, L, C, D>), dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
                        dim3(kWaves * kWave), lds, stream, static_cast<const typename In::raw*>(logits), bias, T, E,
                        k, opt, topk_idx, topk_weights);
     return hipGetLastError();
 }
 
+constexpr int64_t kRowTokens = 2048;    // tokens from which a row of 16 lanes takes one
+
 template <typename In>
 hipError_t launch_type(const void* logits, const float* bias, int64_t T, int E, int k, const RouteOptions& opt,
                        int64_t* topk_idx, float* topk_weights, hipStream_t stream) {
-    if (E <= 64) return launch_lc<In, 64, 1>(logits, bias, T, E, k, opt, topk_idx, topk_weights, stream);
-    if (E <= 256) return launch_lc<In, 64, 4>(logits, bias, T, E, k, opt, topk_idx, topk_weights, stream);
-    if (E <= 512) return launch_lc<In, 64, 8>(logits, bias, T, E, k, opt, topk_idx, topk_weights, stream);
-    return launch_lc<In, 64, 32>(logits, bias, T, E, k, opt, topk_idx, topk_weights, stream);
+#define EP_ROUTE(L, C, D) launch_lanes<In, L, C, D>(logits, bias, T, E, k, opt, topk_idx, topk_weights, stream)
+    // 16 lanes a token have a quarter of the instructions a token; 64 lanes the
+    // shorter way through one.
+    if (T >= kRowTokens && k <= 16) {
+        if (E <= 64) return EP_ROUTE(16, 4, 4);
+        if (E <= 128) return EP_ROUTE(16, 8, 8);
+        if (E <= 256) return k <= 8 ? EP_ROUTE(16, 16, 8) : EP_ROUTE(16, 16, 16);
+    }
+    if (E <= 64) return EP_ROUTE(64, 1, 1);
+    if (E <= 256) return EP_ROUTE(64, 4, 4);
+    if (E <= 512) return EP_ROUTE(64, 8, 8);
+    if (E <= 1024) return EP_ROUTE(64, 16, 16);
+    return EP_ROUTE(64, 32, 32);
+#undef EP_ROUTE
 }
 
 template <typename In>
