@@ -224,8 +224,10 @@ __device__ __forceinline__ float group_score(Best b, int group_top) {
     return group_top == 2 && b.second > -kInf ? b.first + b.second : b.first;
 }
 
-// D: how far down a lane's list k rounds can get, min(C, k) or more.
-template <typename In, int L, int C, int D>
+// D: how far down a lane's list k rounds can get, min(C, k) or more.  kByChoice:
+// by 64-bit scores and bias, else by the logits (a kernel of its own: half the
+// registers, so twice the waves).
+template <typename In, int L, int C, int D, bool kByChoice>
 __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In::raw* __restrict__ logits,
                                                               const float* __restrict__ bias, int64_t T,
                                                               int E, int k, RouteOptions opt,
@@ -235,10 +237,9 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In:
     extern __shared__ float choices[];              // [kWaves * kTokens][E], groups of other sizes only
     const int lane = lane_id(), pos = lane % L, sub = lane / L;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const bool by_choice = bias || (opt.num_groups > 1 && opt.group_top == 2);
     const int e0 = pos * C, size = E / opt.num_groups;
     float b[C] = {};
-    if (bias) {
+    if (kByChoice && bias) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
             if (e0 + c < E) b[c] = bias[e0 + c];
@@ -259,7 +260,7 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In:
         float choice[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) choice[c] = l[c];
-        if (by_choice) {
+        if (kByChoice) {
             // fl32 of the 64-bit score: an fp32 one is off by a step or two, enough
             // to put neighbours in another order.
             if (opt.sigmoid) {
@@ -361,7 +362,7 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In:
         const bool filled = pos < k && is_key(won);
         const int e = filled ? key_expert(won) : -1;
         float le = -kInf;
-        if (filled) le = by_choice ? logit<In>(logits + t * E + e) : key_choice(won);
+        if (filled) le = kByChoice ? logit<In>(logits + t * E + e) : key_choice(won);
         float a, total = 1.0f;
         if (opt.sigmoid) {
             const float low = opt.renormalize ? fminf(max_over<L>(le), 0.0f) : 0.0f;
@@ -388,72 +389,132 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In:
     }
 }
 
-// One wave per token: lane j takes slot j, the slots' contributions meet in a
-// row of the block's memory, and the whole wave writes the row out.
-template <typename In>
+// The value of lane i of the token's lanes, in all of them.
+template <int L>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int i) {
+    if (L == 64) return __builtin_amdgcn_readlane(v, i);
+    switch (i) {                                    // i is a constant where this is called: row_newbcast
+#define EP_LANE(n) \
+    case n: return __builtin_amdgcn_update_dpp(0, v, 0x150 + n, 0xF, 0xF, true);
+        EP_LANE(0) EP_LANE(1) EP_LANE(2) EP_LANE(3) EP_LANE(4) EP_LANE(5) EP_LANE(6) EP_LANE(7)
+        EP_LANE(8) EP_LANE(9) EP_LANE(10) EP_LANE(11) EP_LANE(12) EP_LANE(13) EP_LANE(14) EP_LANE(15)
+#undef EP_LANE
+    }
+    return 0;
+}
+
+// ---- gradient --------------------------------------------------------------------
+// Tokens and experts to lanes as above; lane j also takes slot j.  The slots'
+// contributions meet in a row of the block's memory, from which every lane takes
+// those of its experts: bound by writing [T, E] (and reading it, kDense: softmax
+// not renormalised, where every element has a gradient).
+template <typename In, int L, int C, bool kDense>
 __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(
     const typename In::raw* __restrict__ logits, const int64_t* __restrict__ topk_idx,
     const float* __restrict__ grad_weights, int64_t T, int E, int k, bool is_sigmoid, bool renormalize,
     float scale, typename In::raw* __restrict__ grad_logits) {
-    extern __shared__ float rows[];                 // [kWaves][E]
-    const int lane = lane_id();
+    constexpr int kTokens = kWave / L, kPiece = C < 4 ? C : 4;
+    typedef float Piece __attribute__((ext_vector_type(kPiece)));
+    typedef typename In::raw Vector __attribute__((ext_vector_type(C), aligned(sizeof(typename In::raw))));
+    // [token][piece c / 4 of a lane][lane]: what a lane reads at once lies together.
+    __shared__ Piece rows[kWaves * kTokens][C / kPiece][L];
+    const int lane = lane_id(), pos = lane % L, sub = lane / L;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    float* row = rows + wave * E;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWaves + wave; t < T; t += step) {
+    const int e0 = pos * C;
+    Piece(*row)[L] = rows[wave * kTokens + sub];
+    float* flat = reinterpret_cast<float*>(row);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kTokens;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTokens; t0 < T; t0 += step) {
+        const bool live = t0 + sub < T;
+        const int64_t t = live ? t0 + sub : T - 1;  // lanes past the end repeat the last token
         const typename In::raw* in = logits + t * E;
+        float l[C];
+        if (kDense) load_logits<In, C>(in + e0, E - e0, l);
         int e = -1;
-        float g = 0.0f, l = -kInf;
-        if (lane < k) {
-            const int64_t id = topk_idx[t * k + lane];
+        float g = 0.0f, le = -kInf;
+        if (pos < k) {
+            const int64_t id = topk_idx[t * k + pos];
+            g = grad_weights[t * k + pos];
             if (id >= 0 && id < E) {
                 e = static_cast<int>(id);
-                g = grad_weights[t * k + lane];
-                l = logit<In>(in + e);
+                le = logit<In>(in + e);
             }
         }
-        const bool dense = !is_sigmoid && !renormalize;
-        float top = -kInf, total = 0.0f;
-        if (dense) {
-            for (int i = lane; i < E; i += kWave) top = fmaxf(top, logit<In>(in + i));
-            top = max_over<kWave>(top);
-            for (int i = lane; i < E; i += kWave) total += softmax_term(logit<In>(in + i), top);
-            total = sum_over<kWave>(total);
+        if (le == -kInf) {                          // unavailable: no score, no gradient
+            g = 0.0f;
+            e = -1;
         }
-        float d, mean = 0.0f;                       // this slot's contribution
-        if (l == -kInf) g = 0.0f;                   // unavailable: no score, no gradient
-        if (dense) {
-            const float s = total > 0.0f ? softmax_term(l, top) / total : 0.0f;
-            mean = sum_over<kWave>(g * s);
+        // This slot's contribution d; kDense: to the sum in s (d - mean), else as it is.
+        float d, mean = 0.0f;
+        if (kDense) {
+            float top = -kInf, total = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) top = fmaxf(top, l[c]);
+            top = max_over<L>(top);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                // 2^x of the hardware: off by a step and by 2.5 units of l - top, and
+                // the rounding of the exponent's argument is the larger part of that.
+                l[c] = l[c] == top ? (top > -kInf ? 1.0f : 0.0f)
+                                   : __builtin_amdgcn_exp2f((l[c] - top) * 1.44269504f);
+                total += l[c];
+            }
+            total = sum_over<L>(total);
+            const float inverse = total > 0.0f ? scale / total : 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) l[c] *= inverse;            // scale * s
             d = g;
+            mean = sum_over<L>(e >= 0 ? g * (softmax_term(le, top) / total) : 0.0f);
         } else if (renormalize) {
-            const float m = max_over<kWave>(l);
-            const float a = is_sigmoid ? sigmoid_over(l, fminf(m, 0.0f)) : softmax_term(l, m);
-            const float sum = sum_over<kWave>(a);
+            const float m = max_over<L>(le);
+            const float a = is_sigmoid ? sigmoid_over(le, fminf(m, 0.0f)) : softmax_term(le, m);
+            const float sum = sum_over<L>(a);
             const float p = sum > 0.0f ? a / sum : 0.0f;
-            mean = sum_over<kWave>(g * p);
-            d = p * (g - mean);
-            if (is_sigmoid) d *= sigmoid(-l);
+            d = scale * p * (g - sum_over<L>(g * p));
+            if (is_sigmoid) d *= sigmoid(-le);
         } else {
-            d = g * sigmoid(l) * sigmoid(-l);
+            d = scale * g * sigmoid(le) * sigmoid(-le);
         }
         // Slots of the same expert add in slot order, whichever lane writes.
         float all = 0.0f;
-        for (int j = 0; j < k; ++j)
-            if (read_lane(e, j) == e) all += read_lane(d, j);
-        for (int i = lane; i < E; i += kWave) row[i] = 0.0f;
-        __builtin_amdgcn_wave_barrier();
-        if (e >= 0 && l > -kInf) row[e] = all;
-        __builtin_amdgcn_wave_barrier();
-        for (int i = lane; i < E; i += kWave) {
-            float v = row[i];
-            if (dense) {
-                const float s = total > 0.0f ? softmax_term(logit<In>(in + i), top) / total : 0.0f;
-                v = s * (v - mean);
+        if (L == 64) {
+            for (int j = 0; j < k; ++j)
+                if (read_lane(e, j) == e) all += read_lane(d, j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (j >= k) break;
+                const int o = static_cast<int>(from_lane<L>(static_cast<uint32_t>(e), j));
+                const float v = __uint_as_float(from_lane<L>(__float_as_uint(d), j));
+                all += o == e ? v : 0.0f;
             }
-            grad_logits[t * E + i] = from_float(In(), scale * v);
+        }
+#pragma unroll
+        for (int i = 0; i < C / kPiece; ++i) row[i][pos] = Piece{};
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (e >= 0) flat[(e % C / kPiece * L + e / C) * kPiece + e % kPiece] = all;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        Vector out;
+#pragma unroll
+        for (int i = 0; i < C / kPiece; ++i) {
+            const Piece v = row[i][pos];
+#pragma unroll
+            for (int c = 0; c < kPiece; ++c)
+                out[i * kPiece + c] = from_float(In(), kDense ? l[i * kPiece + c] * (v[c] - mean) : v[c]);
         }
         __builtin_amdgcn_wave_barrier();
+        if (live) {
+            typename In::raw* to = grad_logits + t * E + e0;
+            if (e0 + C <= E) {
+                *reinterpret_cast<Vector*>(to) = out;
+            } else {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (e0 + c < E) to[c] = out[c];
+            }
+        }
     }
 }
 
@@ -462,22 +523,30 @@ hipError_t launch_lanes(const void* logits, const float* bias, int64_t T, int E,
                         int64_t* topk_idx, float* topk_weights, hipStream_t stream) {
     const int per_block = kWaves * (kWave / L);
     const int64_t blocks = ceil_div(T, per_block), cap = kMaxLaunchThreads / (kWaves * kWave);
+    const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap)), block(kWaves * kWave);
     const size_t lds = opt.num_groups > 1 ? sizeof(float) * per_block * E : 0;
-    hipLaunchKernelGGL((route_kernel<In, L, C, D>), dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
-                       dim3(kWaves * kWave), lds, stream, static_cast<const typename In::raw*>(logits), bias, T, E,
-                       k, opt, topk_idx, topk_weights);
+    const typename In::raw* in = static_cast<const typename In::raw*>(logits);
+    if (bias || (opt.num_groups > 1 && opt.group_top == 2))
+        hipLaunchKernelGGL((route_kernel<In, L, C, D, true>), grid, block, lds, stream, in, bias, T, E, k, opt,
+                           topk_idx, topk_weights);
+    else
+        hipLaunchKernelGGL((route_kernel<In, L, C, D, false>), grid, block, lds, stream, in, bias, T, E, k, opt,
+                           topk_idx, topk_weights);
     return hipGetLastError();
 }
 
-constexpr int64_t kRowTokens = 2048;    // tokens from which a row of 16 lanes takes one
+// Tokens from which a row of 16 lanes takes one: it has a quarter of the
+// instructions a token, 64 lanes the shorter way through one.  Measured, 64 lanes
+// against 16 (us): 256 experts, top 8, 4.2 / 5.2 at 2048 tokens, 5.9 / 5.4 at 4096,
+// 27.8 / 17.6 at 32768; 128 experts, top 4, 3.6 / 3.9 at 2048, 4.8 / 3.8 at 4096;
+// 64 experts, top 6, 2.9 / 3.1 at 1024, 3.3 / 3.2 at 2048.
+int64_t row_tokens(int E) { return E > 128 ? 4096 : 2048; }
 
 template <typename In>
 hipError_t launch_type(const void* logits, const float* bias, int64_t T, int E, int k, const RouteOptions& opt,
                        int64_t* topk_idx, float* topk_weights, hipStream_t stream) {
 #define EP_ROUTE(L, C, D) launch_lanes<In, L, C, D>(logits, bias, T, E, k, opt, topk_idx, topk_weights, stream)
-    // 16 lanes a token have a quarter of the instructions a token; 64 lanes the
-    // shorter way through one.
-    if (T >= kRowTokens && k <= 16) {
+    if (T >= row_tokens(E) && k <= 16) {
         if (E <= 64) return EP_ROUTE(16, 4, 4);
         if (E <= 128) return EP_ROUTE(16, 8, 8);
         if (E <= 256) return k <= 8 ? EP_ROUTE(16, 16, 8) : EP_ROUTE(16, 16, 16);
@@ -490,16 +559,41 @@ hipError_t launch_type(const void* logits, const float* bias, int64_t T, int E, 
 #undef EP_ROUTE
 }
 
+template <typename In, int L, int C>
+hipError_t launch_back_lanes(const void* logits, const int64_t* topk_idx, const float* grad_weights, int64_t T,
+                             int E, int k, bool is_sigmoid, bool renormalize, float scale, void* grad_logits,
+                             hipStream_t stream) {
+    const int64_t blocks = ceil_div(T, kWaves * (kWave / L)), cap = kMaxLaunchThreads / (kWaves * kWave);
+    const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap)), block(kWaves * kWave);
+    const typename In::raw* in = static_cast<const typename In::raw*>(logits);
+    typename In::raw* out = static_cast<typename In::raw*>(grad_logits);
+    if (!is_sigmoid && !renormalize)
+        hipLaunchKernelGGL((route_backward_kernel<In, L, C, true>), grid, block, 0, stream, in, topk_idx,
+                           grad_weights, T, E, k, is_sigmoid, renormalize, scale, out);
+    else
+        hipLaunchKernelGGL((route_backward_kernel<In, L, C, false>), grid, block, 0, stream, in, topk_idx,
+                           grad_weights, T, E, k, is_sigmoid, renormalize, scale, out);
+    return hipGetLastError();
+}
+
 template <typename In>
 hipError_t launch_back(const void* logits, const int64_t* topk_idx, const float* grad_weights, int64_t T, int E,
                        int k, bool is_sigmoid, bool renormalize, float scale, void* grad_logits,
                        hipStream_t stream) {
-    const int64_t blocks = ceil_div(T, kWaves), cap = kMaxLaunchThreads / (kWaves * kWave);
-    hipLaunchKernelGGL((route_backward_kernel<In>), dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
-                       dim3(kWaves * kWave), sizeof(float) * kWaves * E, stream,
-                       static_cast<const typename In::raw*>(logits), topk_idx, grad_weights, T, E, k, is_sigmoid,
-                       renormalize, scale, static_cast<typename In::raw*>(grad_logits));
-    return hipGetLastError();
+#define EP_BACK(L, C)                                                                                        \
+    launch_back_lanes<In, L, C>(logits, topk_idx, grad_weights, T, E, k, is_sigmoid, renormalize, scale,     \
+                                grad_logits, stream)
+    if (T >= row_tokens(E) && k <= 16) {
+        if (E <= 64) return EP_BACK(16, 4);
+        if (E <= 128) return EP_BACK(16, 8);
+        if (E <= 256) return EP_BACK(16, 16);
+    }
+    if (E <= 64) return EP_BACK(64, 1);
+    if (E <= 256) return EP_BACK(64, 4);
+    if (E <= 512) return EP_BACK(64, 8);
+    if (E <= 1024) return EP_BACK(64, 16);
+    return EP_BACK(64, 32);
+#undef EP_BACK
 }
 
 }  // namespace
