@@ -4,8 +4,7 @@
 // the gradient back.
 //
 // Choosing.  L lanes of a wave hold one token (64 / L tokens a wave), C of its
-// experts each, in order: lane p has experts C p .. C p + C - 1.  A choice and its
-// expert make one 64-bit key that is also a positive double, so that one
+// experts each.  A choice and its expert make one 64-bit key that is also a positive double, so that one
 // instruction (v_max_f64, as fast as an fp32 one here) compares both, ties
 // included.  Every lane sorts its keys once (a network of v_max / v_min); each of
 // the k rounds is then a maximum over the lanes' first keys, and the lane that
@@ -30,7 +29,9 @@ __device__ __forceinline__ float to_float(F32, float v) { return v; }
 __device__ __forceinline__ float to_float(Bf16, uint16_t v) { return bf16_lo(v); }
 __device__ __forceinline__ float to_float(F16, _Float16 v) { return static_cast<float>(v); }
 __device__ __forceinline__ float from_float(F32, float v) { return v; }
-__device__ __forceinline__ uint16_t from_float(Bf16, float v) { return static_cast<uint16_t>(bf16_rne(v)); }
+__device__ __forceinline__ uint16_t from_float(Bf16, float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));       // to nearest, ties to even
+}
 __device__ __forceinline__ _Float16 from_float(F16, float v) { return static_cast<_Float16>(v); }
 
 // An unavailable expert's logit reads as -inf.
@@ -193,26 +194,56 @@ __device__ __forceinline__ void sort_keys(double (&k)[C]) {
                 }
 }
 
-// The C logits from p on, of which the first n exist, and -inf for the others.
-template <typename In, int C>
-__device__ __forceinline__ void load_logits(const typename In::raw* p, int n, float (&l)[C]) {
-    // (Elements may lie anywhere: global loads need no alignment.)
-    typedef typename In::raw Vector __attribute__((ext_vector_type(C), aligned(sizeof(typename In::raw))));
-    if (n >= C) {
-        const Vector v = *reinterpret_cast<const Vector*>(p);
-#pragma unroll
-        for (int c = 0; c < C; ++c) l[c] = to_float(In(), v[c]);
-    } else {
-#pragma unroll
-        for (int c = 0; c < C; ++c) l[c] = c < n ? to_float(In(), p[c]) : -kInf;
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (l[c] != l[c]) l[c] = -kInf;
-}
+// Which experts a lane holds: pieces of P in a row, 16 bytes where C allows,
+// piece i from expert a i + b pos on.  Interleaved, the lanes' pieces lie side by
+// side, as loads and stores want them; in order, a lane's pieces do, as groups of
+// experts want them.
+template <typename In, int L, int C>
+struct Layout {
+    static constexpr int kFull = 16 / static_cast<int>(sizeof(typename In::raw)), P = C < kFull ? C : kFull;
+    // (Elements may lie anywhere: global accesses need no alignment.)
+    typedef typename In::raw Vector __attribute__((ext_vector_type(P), aligned(sizeof(typename In::raw))));
+    int a, b;
+    __device__ __forceinline__ explicit Layout(bool in_order) : a(in_order ? P : L * P), b(in_order ? C : P) {}
+    __device__ __forceinline__ int expert(int c, int pos) const { return c / P * a + pos * b + c % P; }
 
-// Whether the calling lane's experts are in a kept group, where every group is a
-// power of two of whole lanes: kept[c] for each.
+    // A token's logits, -inf for experts that do not exist.
+    __device__ __forceinline__ void load(const typename In::raw* in, int pos, int E, float (&l)[C]) const {
+#pragma unroll
+        for (int i = 0; i < C / P; ++i) {
+            const int e = i * a + pos * b;
+            if (e + P <= E) {
+                const Vector v = *reinterpret_cast<const Vector*>(in + e);
+#pragma unroll
+                for (int c = 0; c < P; ++c) l[i * P + c] = to_float(In(), v[c]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < P; ++c) l[i * P + c] = e + c < E ? to_float(In(), in[e + c]) : -kInf;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (l[c] != l[c]) l[c] = -kInf;
+    }
+    __device__ __forceinline__ void store(typename In::raw* out, int pos, int E, const float (&v)[C]) const {
+#pragma unroll
+        for (int i = 0; i < C / P; ++i) {
+            const int e = i * a + pos * b;
+            Vector o;
+#pragma unroll
+            for (int c = 0; c < P; ++c) o[c] = from_float(In(), v[i * P + c]);
+            if (e + P <= E) {
+                *reinterpret_cast<Vector*>(out + e) = o;
+            } else {
+#pragma unroll
+                for (int c = 0; c < P; ++c)
+                    if (e + c < E) out[e + c] = o[c];
+            }
+        }
+    }
+};
+
+// The two best of a group.
 struct Best {
     float first, second;                            // -inf: none
 };
@@ -237,19 +268,20 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In:
     extern __shared__ float choices[];              // [kWaves * kTokens][E], groups of other sizes only
     const int lane = lane_id(), pos = lane % L, sub = lane / L;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const int e0 = pos * C, size = E / opt.num_groups;
+    const int size = E / opt.num_groups;
+    const Layout<In, L, C> layout(opt.num_groups > 1);
     float b[C] = {};
     if (kByChoice && bias) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (e0 + c < E) b[c] = bias[e0 + c];
+            if (layout.expert(c, pos) < E) b[c] = bias[layout.expert(c, pos)];
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kTokens;
     for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTokens; t0 < T; t0 += step) {
         const bool live = t0 + sub < T;
         const int64_t t = live ? t0 + sub : T - 1;  // lanes past the end repeat the last token
         float l[C];
-        load_logits<In, C>(logits + t * E + e0, E - e0, l);
+        layout.load(logits + t * E, pos, E, l);
         float top = -kInf;
         if (!opt.sigmoid) {
 #pragma unroll
@@ -306,7 +338,7 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In:
                 float* row = choices + (wave * kTokens + sub) * E;
 #pragma unroll
                 for (int c = 0; c < C; ++c)
-                    if (e0 + c < E) row[e0 + c] = choice[c];
+                    if (layout.expert(c, pos) < E) row[layout.expert(c, pos)] = choice[c];
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
                 float mine[kWave / L];
@@ -337,13 +369,13 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(const typename In:
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll
                 for (int c = 0; c < C; ++c)
-                    if (e0 + c < E && !(kept >> ((e0 + c) / size) & 1)) choice[c] = -kInf;
+                    if (layout.expert(c, pos) < E && !(kept >> (layout.expert(c, pos) / size) & 1)) choice[c] = -kInf;
             }
         }
 
         double key[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) key[c] = make_key(choice[c], e0 + c);
+        for (int c = 0; c < C; ++c) key[c] = make_key(choice[c], layout.expert(c, pos));
         sort_keys<C>(key);
         // k rounds: the largest first key of the token's lanes goes to lane j, and
         // the lane that had it moves up.
@@ -413,14 +445,13 @@ __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(
     const typename In::raw* __restrict__ logits, const int64_t* __restrict__ topk_idx,
     const float* __restrict__ grad_weights, int64_t T, int E, int k, bool is_sigmoid, bool renormalize,
     float scale, typename In::raw* __restrict__ grad_logits) {
-    constexpr int kTokens = kWave / L, kPiece = C < 4 ? C : 4;
+    constexpr int kTokens = kWave / L, P = Layout<In, L, C>::P, kPiece = P < 4 ? P : 4;
     typedef float Piece __attribute__((ext_vector_type(kPiece)));
-    typedef typename In::raw Vector __attribute__((ext_vector_type(C), aligned(sizeof(typename In::raw))));
     // [token][piece c / 4 of a lane][lane]: what a lane reads at once lies together.
     __shared__ Piece rows[kWaves * kTokens][C / kPiece][L];
     const int lane = lane_id(), pos = lane % L, sub = lane / L;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const int e0 = pos * C;
+    const Layout<In, L, C> layout(false);
     Piece(*row)[L] = rows[wave * kTokens + sub];
     float* flat = reinterpret_cast<float*>(row);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kTokens;
@@ -429,7 +460,7 @@ __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(
         const int64_t t = live ? t0 + sub : T - 1;  // lanes past the end repeat the last token
         const typename In::raw* in = logits + t * E;
         float l[C];
-        if (kDense) load_logits<In, C>(in + e0, E - e0, l);
+        if (kDense) layout.load(in, pos, E, l);
         int e = -1;
         float g = 0.0f, le = -kInf;
         if (pos < k) {
@@ -493,28 +524,22 @@ __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(
         for (int i = 0; i < C / kPiece; ++i) row[i][pos] = Piece{};
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (e >= 0) flat[(e % C / kPiece * L + e / C) * kPiece + e % kPiece] = all;
+        if (e >= 0) {
+            const int c = e / (L * P) * P + e % P;  // of lane e / P mod L
+            flat[(c / kPiece * L + e / P % L) * kPiece + c % kPiece] = all;
+        }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        Vector out;
+        float out[C];
 #pragma unroll
         for (int i = 0; i < C / kPiece; ++i) {
             const Piece v = row[i][pos];
 #pragma unroll
             for (int c = 0; c < kPiece; ++c)
-                out[i * kPiece + c] = from_float(In(), kDense ? l[i * kPiece + c] * (v[c] - mean) : v[c]);
+                out[i * kPiece + c] = kDense ? l[i * kPiece + c] * (v[c] - mean) : v[c];
         }
         __builtin_amdgcn_wave_barrier();
-        if (live) {
-            typename In::raw* to = grad_logits + t * E + e0;
-            if (e0 + C <= E) {
-                *reinterpret_cast<Vector*>(to) = out;
-            } else {
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (e0 + c < E) to[c] = out[c];
-            }
-        }
+        if (live) layout.store(grad_logits + t * E, pos, E, out);
     }
 }
 
@@ -537,10 +562,14 @@ hipError_t launch_lanes(const void* logits, const float* bias, int64_t T, int E,
 
 // Tokens from which a row of 16 lanes takes one: it has a quarter of the
 // instructions a token, 64 lanes the shorter way through one.  Measured, 64 lanes
-// against 16 (us): 256 experts, top 8, 4.2 / 5.2 at 2048 tokens, 5.9 / 5.4 at 4096,
-// 27.8 / 17.6 at 32768; 128 experts, top 4, 3.6 / 3.9 at 2048, 4.8 / 3.8 at 4096;
-// 64 experts, top 6, 2.9 / 3.1 at 1024, 3.3 / 3.2 at 2048.
+// against 16 (us): 256 experts, top 8, 4.1 / 5.3 at 2048 tokens, 5.7 / 5.5 at 4096,
+// 27.6 / 18.6 at 32768; 128 experts, top 4, 3.6 / 3.7 at 2048, 4.9 / 3.8 at 4096;
+// 64 experts, top 6, 2.9 / 3.1 at 1024, 3.3 / 3.1 at 2048.  The gradient has fewer
+// instructions to save: 256 experts 5.3 / 5.5 at 8192, 13.6 / 11.7 at 32768 (fp32,
+// softmax), 16.4 / 13.2 (bf16, every logit); 64 experts 3.2 / 3.5 at 4096, 4.2 / 3.7
+// at 8192.
 int64_t row_tokens(int E) { return E > 128 ? 4096 : 2048; }
+int64_t row_tokens_back(int E) { return E > 128 ? 12288 : 6144; }
 
 template <typename In>
 hipError_t launch_type(const void* logits, const float* bias, int64_t T, int E, int k, const RouteOptions& opt,
@@ -583,7 +612,7 @@ hipError_t launch_back(const void* logits, const int64_t* topk_idx, const float*
 #define EP_BACK(L, C)                                                                                        \
     launch_back_lanes<In, L, C>(logits, topk_idx, grad_weights, T, E, k, is_sigmoid, renormalize, scale,     \
                                 grad_logits, stream)
-    if (T >= row_tokens(E) && k <= 16) {
+    if (T >= row_tokens_back(E) && k <= 16) {
         if (E <= 64) return EP_BACK(16, 4);
         if (E <= 128) return EP_BACK(16, 8);
         if (E <= 256) return EP_BACK(16, 16);
