@@ -24,7 +24,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
 constexpr int kTileRows = 128, kTileWeights = 512, kTileThreads = 512;
-constexpr int kSplitBelow = 2;      // items a block below which its waves split each item
 
 // Eight codes of one word, times the scale 2^(b - 127) whose bits are b << 23.
 __device__ __forceinline__ bf16x8 decode(uint32_t codes, float scale) {
@@ -202,13 +201,28 @@ __device__ __forceinline__ uint32_t code_offset(const Operands& o, int n, int N,
 // ---- few rows per expert: bound by reading the weights ---------------------------
 // A wave takes 64 weight rows (kSilu: 32 gate rows and their 32 up rows) and up
 // to 16 token rows, 256 inputs at a time: whole 128-byte lines of the codes (64
-// bytes of twice as many rows is a fifth slower from HBM) and, kEven, their eight
-// scales in one load (byte loads cost a quarter of the whole).  Where there are
-// items for every wave, each takes whole items; where there are not (a single
-// token's eight experts), the four waves of a block split an item's inputs, so
-// that every CU has loads in flight, and join their sums in shared memory in wave
-// order.  Nothing is staged: the four waves of a block read the same token rows,
-// which the L1 holds, and never wait for each other.
+// bytes of twice as many rows is a fifth slower from HBM).  Where there are items
+// for every wave, each takes whole items; where there are not (a single token's
+// eight experts), the four waves of a block split an item's inputs, so that every
+// CU has loads in flight, and join their sums in shared memory in wave order.  No
+// codes or token rows are staged: the four waves of a block read the same token
+// rows, which the L1 holds, and never wait for each other.
+//
+// The scales are a sixteenth of the codes' bytes, but 8 bytes of every row a step:
+// lines that the codes have driven out of the L1 by the next step.  An item's
+// scale rows lie together in memory, so they come into shared memory once, in
+// whole loads, where K <= kSharedScales and K % 512 == 0; else each step loads
+// eight of a row (K % 256 == 0) or single ones.  (128 experts of one row, 7168 ->
+// 2 x 2048, 2.0 GB: 345 us, 5.8 TB/s, against 432 with eight a load; 256 experts of
+// 4 rows, 2048 -> 7168, 2.0 GB: 406 against 446, of 16 rows 525 against 545.)
+enum Scales { kSingle, kEight, kShared };
+constexpr int kSharedScales = 8192;
+
+// 16-byte places of an item's block of scale rows, in whole loads of 64.
+template <bool kSilu>
+__device__ __forceinline__ int scale_slots(int K) {
+    return ((kSilu ? 32 : 64) * (K / 512) + 63) / 64 * 64;
+}
 
 // Register s of the lanes of group q (lane / 16) and register q of group s change
 // places: halves of the wave first, then neighbouring groups.
@@ -226,10 +240,11 @@ __device__ __forceinline__ void transpose_groups(u32x4 (&v)[4]) {
     }
 }
 
-// acc += the products over inputs k, k + step, ...  kEven: K % 256 == 0.
-template <bool kSilu, bool kEven>
+// acc += the products over inputs k, k + step, ...  kShared: scale_rows has the
+// item's, and is being filled: `join` are the waves that fill it together.
+template <bool kSilu, Scales kScales>
 __device__ __forceinline__ void stream_products(const Operands& o, int k, int step, int K, int N, int q, int i16,
-                                                f32x4* acc) {
+                                                const uint8_t* scale_rows, bool join, f32x4* acc) {
     uint32_t cr[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) cr[j] = code_offset(o, (kSilu ? j % 2 : j) * 16 + i16, N, K, q);
@@ -241,17 +256,17 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
     // for all that is on the way.
     auto load = [&](int buf, int at) {
         at = at < K ? at : K - 128;
-        const int more = kEven || at + 128 < K ? 128 : 0;
-        if (kEven && at + 128 >= K) at = K - 256;
+        const int more = kScales != kSingle || at + 128 < K ? 128 : 0;
+        if (kScales != kSingle && at + 128 >= K) at = K - 256;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const Buffer wb = o.wb[kSilu ? j / 2 : 0], sb = o.sb[kSilu ? j / 2 : 0];
             w[buf][0][j] = load16(wb, cr[j], at / 2);
             w[buf][1][j] = load16(wb, cr[j], (at + more) / 2);
-            if (kEven) {
-                // The line of scales starts where group 0's lane has its own.
+            if (kScales == kEight) {
+                // A row's scales of this step start where group 0's lane has its own.
                 b[buf][j] = load8(sb, cr[j] / 16 - q, at / 32);
-            } else {
+            } else if (kScales == kSingle) {
                 b[buf][j][0] = load1(sb, cr[j] / 16, at / 32);
                 b[buf][j][1] = load1(sb, cr[j] / 16, (at + more) / 32);
             }
@@ -270,7 +285,7 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
         float scale[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            scale[j] = __uint_as_float((kEven ? b[buf][j][h] >> 8 * q & 0xFF : b[buf][j][h]) << 23);
+            scale[j] = __uint_as_float((kScales != kSingle ? b[buf][j][h] >> 8 * q & 0xFF : b[buf][j][h]) << 23);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -278,42 +293,73 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
                 acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode(w[buf][h][j][s], scale[j]),
                                                                  __builtin_bit_cast(bf16x8, v[h][s]), acc[j], 0, 0, 0);
     };
-    // Loads return in order: token rows are asked for before the weights that may
-    // stay on the way while they are waited for.
+    // Loads return in order: the token rows of a half step are asked for before
+    // what may stay on the way while they are waited for.
     auto pass = [&](int buf, int at) {
-        rows(1, at + 128);
-        __builtin_amdgcn_sched_barrier(0);
-        load(1 - buf, at + step);
-        __builtin_amdgcn_sched_barrier(0);
+        if (kScales == kShared) {
+            const int here = at < K ? at : 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int up = kSilu && j >= 2 ? scale_slots<kSilu>(K) * 16 : 0;
+                const int n = (kSilu ? j % 2 : j) * 16 + i16;
+                b[buf][j] = *reinterpret_cast<const u32x2*>(scale_rows + up + n * (K / 32) + here / 32);
+            }
+        }
         if (at < K) multiply(buf, 0);
         __builtin_amdgcn_sched_barrier(0);
         rows(0, at + step);
         __builtin_amdgcn_sched_barrier(0);
         if (at + 128 < K) multiply(buf, 1);
         __builtin_amdgcn_sched_barrier(0);
+        rows(1, at + step + 128);
+        __builtin_amdgcn_sched_barrier(0);
+        load(buf, at + 2 * step);
+        __builtin_amdgcn_sched_barrier(0);
     };
     load(0, k);
+    __builtin_amdgcn_sched_barrier(0);
     rows(0, k);
+    rows(1, k + 128);
+    __builtin_amdgcn_sched_barrier(0);
+    load(1, k + step);
+    __builtin_amdgcn_sched_barrier(0);
+    if (kScales == kShared) {
+        // Behind the scales: two times eight codes and two times four rows.
+        asm volatile("s_waitcnt vmcnt(24)" ::: "memory");
+        if (join) __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    }
     for (; k < K; k += 2 * step) {
         pass(0, k);
         pass(1, k + step);
     }
 }
 
-template <bool kSilu, bool kEven>
-__global__ __launch_bounds__(kThreads, 3) void stream_w4_kernel(
+template <bool kSilu, Scales kScales>
+__global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
     const uint16_t* __restrict__ x, int64_t num_rows, const int32_t* __restrict__ expert_rows, int capacity,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N, int most,
     uint16_t* __restrict__ y) {
     constexpr int kOut = kSilu ? 32 : 64;           // outputs of an item
-    __shared__ f32x4 part[4][4][kWave];             // [wave][weight tile][lane]
+    constexpr int kRoom = 64 * kSharedScales / 32 / 16;
+    __shared__ u32x4 scale_room[kScales == kShared ? 4 : 1][kScales == kShared ? kRoom : 1];     // a wave's
+    __shared__ f32x4 part_room[kScales == kShared ? 1 : 16][kWave];
     extern __shared__ int32_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const Table t = make_table(room, expert_rows, E, capacity, num_rows, 16, 0, most);
     const int columns = (N + kOut - 1) / kOut;
     const int64_t items = static_cast<int64_t>(t.start[E]) * columns;
-    const bool split = items < kSplitBelow * static_cast<int64_t>(gridDim.x);
+    // Whole items from 1.25 a block on: 8 experts (7168 -> 2 x 2048, 1 item a block)
+    // split 31 us, whole 40; 24 of 64 (4096 -> 2 x 1024, 1.5) 29.5 both; 8 experts
+    // (2048 -> 7168, 1.75) 23 and 17; 16 (7168 -> 2 x 2048, 2) 58 and 48.
+    const bool split = 4 * items < 5 * static_cast<int64_t>(gridDim.x);
+    // Split items have their scales in the first wave's room, the sums of the
+    // waves (16 weight tiles x lanes) in the second's.
+    static_assert(sizeof(f32x4) * 16 * kWave <= sizeof(u32x4) * kRoom, "room for the sums");
+    f32x4(*part)[kWave] = kScales == kShared ? reinterpret_cast<f32x4(*)[kWave]>(scale_room[kScales == kShared ? 1 : 0])
+                                             : part_room;
+    u32x4* mine_scales = scale_room[kScales == kShared && !split ? wave : 0];
     Share mine = share_of(items);
     if (!split) {                                   // neighbouring items to the waves of a block
         mine.at += blockIdx.x / 8 * 3 + wave;
@@ -327,8 +373,22 @@ __global__ __launch_bounds__(kThreads, 3) void stream_w4_kernel(
         const int left = __builtin_amdgcn_readfirstlane(t.count[e] - m0);
         const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
         const Operands o = operands<kSilu>(x, codes, scales, e, row0, left, column * kOut, K, N);
+        if (kScales == kShared) {
+            // Scale rows of 16 P bytes, P = K / 512, one after the other in memory
+            // as here: one block of 64 rows, or two of 32 (kSilu).  Past a block's
+            // or the outputs' last row its last bytes again.  (The wave's, or
+            // behind the barriers below the block's, reads of the item before
+            // are done.)
+            const int slots = scale_slots<kSilu>(K), last = (N - o.n0 < kOut ? N - o.n0 : kOut) * (K / 512) - 1;
+            for (int g = split ? wave : 0; g * 64 < slots * (kSilu ? 2 : 1); g += split ? 4 : 1) {
+                const bool up = kSilu && g * 64 >= slots;
+                const int at = g * 64 + lane - (up ? slots : 0);
+                load_shared(mine_scales + g * 64, o.sb[up ? 1 : 0], (at < last ? at : last) * 16, 0);
+            }
+        }
         f32x4 acc[4] = {};
-        stream_products<kSilu, kEven>(o, split ? wave * 256 : 0, split ? 1024 : 256, K, N, q, i16, acc);
+        stream_products<kSilu, kScales>(o, split ? wave * 256 : 0, split ? 1024 : 256, K, N, q, i16,
+                                        reinterpret_cast<const uint8_t*>(mine_scales), split, acc);
 
         // A lane holds outputs 4 q .. + 3 of token row i16 of each 16 x 16 tile; of
         // split items wave w ends up with weight tile w (kSilu: waves 0 and 1
@@ -336,10 +396,10 @@ __global__ __launch_bounds__(kThreads, 3) void stream_w4_kernel(
         uint16_t* row = y + (row0 + i16) * N;
         if (split) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part[wave][j][lane] = acc[j];
+            for (int j = 0; j < 4; ++j) part[wave * 4 + j][lane] = acc[j];
             __syncthreads();
             auto sum = [&](int j) {
-                return (part[0][j][lane] + part[1][j][lane]) + (part[2][j][lane] + part[3][j][lane]);
+                return (part[j][lane] + part[4 + j][lane]) + (part[8 + j][lane] + part[12 + j][lane]);
             };
             const int n = o.n0 + wave * 16 + 4 * q;
             if (wave * 16 < kOut && i16 < left && n < N) {
@@ -572,17 +632,18 @@ unsigned blocks_for(int64_t items, int64_t full) {
 // Row tiles of `rows` that a map in order can ask for at most.
 int64_t most_tiles(const Call& c, int rows) { return c.num_rows / rows + (c.num_rows < c.E ? c.num_rows : c.E); }
 
-template <bool kSilu, bool kEven>
+template <bool kSilu, Scales kScales>
 hipError_t launch_stream(const Call& c, int most) {
     const int64_t items = most_tiles(c, 16) * ceil_div(c.N, kSilu ? 32 : 64);
-    hipLaunchKernelGGL((stream_w4_kernel<kSilu, kEven>), dim3(blocks_for(items, 256 * 3)), dim3(kThreads),
+    hipLaunchKernelGGL((stream_w4_kernel<kSilu, kScales>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads),
                        table_bytes(c.E), c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows,
                        c.capacity, c.codes, c.scales, c.E, c.K, c.N, most, static_cast<uint16_t*>(c.y));
     return hipGetLastError();
 }
 template <bool kSilu>
 hipError_t launch_stream(const Call& c, int most) {
-    return c.K % 256 == 0 ? launch_stream<kSilu, true>(c, most) : launch_stream<kSilu, false>(c, most);
+    if (c.K % 512 == 0 && c.K <= kSharedScales) return launch_stream<kSilu, kShared>(c, most);
+    return c.K % 256 == 0 ? launch_stream<kSilu, kEight>(c, most) : launch_stream<kSilu, kSingle>(c, most);
 }
 
 template <bool kSilu>
@@ -594,7 +655,11 @@ hipError_t launch_tile(const Call& c, int above) {
     return hipGetLastError();
 }
 
-constexpr int kFew = 16;    // rows of an expert up to which its weights are streamed
+// Rows of an expert up to which its weights are streamed.  Streams against tiles
+// (us): 64 experts, 4096 -> 2 x 1024, of 4 rows 58 / 95, of 16 rows 70 / 95; 256
+// experts, 2048 -> 7168, of 4 rows 406 / 537, of 16 rows 525 / 548.  With two row
+// tiles a wave (to 32 rows) streams took 104 / 97 at 24 rows and 116 / 98 at 32.
+constexpr int kFew = 16;
 
 template <bool kSilu>
 hipError_t launch(const Call& c) {
