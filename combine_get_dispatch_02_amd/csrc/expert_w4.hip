@@ -485,6 +485,8 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     };
     // Past the end the last step is asked for again.
     auto within = [&](int kb) { return kb < K ? kb : K - 128; };
+    // Waves past the last output bring token rows only.
+    const bool idle = o.n0 + wave * (kSilu ? 32 : 64) >= N;
     f32x16 acc[kTiles][2] = {};
     bf16x8 v[kTiles], a[2];
     auto read = [&](const u32x4* from, int first, int i, int us) {
@@ -506,6 +508,12 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     // are read when its last product is under way.  The barriers to
     // scheduling keep all that in place.
     auto multiply = [&](const u32x4* from, const u32x4* then, u32x4* to, int buf, int kb) {
+        if (idle) {
+            arrive<kFill>();                        // behind the next step's rows, one step's
+#pragma unroll
+            for (int g = 0; g < kFill; ++g) ask_rows(g, to, within(kb + 384));
+            return;
+        }
         // Place 4 h of row i32, from which the others differ by an exclusive or:
         // worked out anew from one register, which the compiler may not see
         // through, or it keeps one for every place.
@@ -537,8 +545,10 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     };
     static_assert(kFill <= 7, "rows are asked for in the last seven groups");
     arrive<0>();                                // the last item's loads and reads are done
+    if (!idle) {
 #pragma unroll
-    for (int g = 0; g < 6; ++g) ask_weights(g, 0, 0);
+        for (int g = 0; g < 6; ++g) ask_weights(g, 0, 0);
+    }
 #pragma unroll
     for (int g = 0; g < kFill; ++g) ask_rows(g, s0, 0);
 #pragma unroll
@@ -546,9 +556,11 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
 #pragma unroll
     for (int g = 0; g < kFill; ++g) ask_rows(g, s2, within(256));
     arrive<2 * kFill>();
-    a[0] = decode_tile(0, 0, 0);
+    if (!idle) {
+        a[0] = decode_tile(0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) read(s0, i32 * 16 + place_of(i32, 4 * h), i, 0);
+        for (int i = 0; i < kTiles; ++i) read(s0, i32 * 16 + place_of(i32, 4 * h), i, 0);
+    }
     int kb = 0;
     for (; kb + 512 <= K; kb += 512) {
         multiply(s0, s1, s3, 0, kb);
@@ -587,18 +599,18 @@ template <bool kSilu>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_w4_kernel(
     const uint16_t* __restrict__ x, int64_t num_rows, const int32_t* __restrict__ expert_rows, int capacity,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int E, int K, int N, int above,
-    uint16_t* __restrict__ y) {
+    int tile_rows, uint16_t* __restrict__ y) {
     constexpr int kOut = kSilu ? kTileWeights / 2 : kTileWeights;
     __shared__ u32x4 s0[kTileRows * 16], s1[kTileRows * 16], s2[kTileRows * 16], s3[kTileRows * 16];
     extern __shared__ int32_t room[];
-    const Table t = make_table(room, expert_rows, E, capacity, num_rows, kTileRows, above, INT32_MAX);
+    const Table t = make_table(room, expert_rows, E, capacity, num_rows, tile_rows, above, INT32_MAX);
     const int columns = (N + kOut - 1) / kOut;
     const Share mine = share_of(static_cast<int64_t>(t.start[E]) * columns);
     for (int64_t item = mine.at; item < mine.end; item += mine.step) {
         const int tile = static_cast<int>(item / columns);
         const int e = expert_of(t, E, tile);
-        const int m0 = (tile - t.start[e]) * kTileRows;
-        const int left = __builtin_amdgcn_readfirstlane(t.count[e] - m0);
+        const int m0 = (tile - t.start[e]) * tile_rows, rest = t.count[e] - m0;
+        const int left = __builtin_amdgcn_readfirstlane(rest < tile_rows ? rest : tile_rows);
         const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
         const Operands o = operands<kSilu>(x, codes, scales, e, row0, left,
                                            static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut, K, N);
@@ -648,10 +660,18 @@ hipError_t launch_stream(const Call& c, int most) {
 
 template <bool kSilu>
 hipError_t launch_tile(const Call& c, int above) {
-    const int64_t items = most_tiles(c, kTileRows) * ceil_div(c.N, kSilu ? kTileWeights / 2 : kTileWeights);
+    // Smaller tiles where they all run at once and those of 128 rows would leave
+    // CUs without one (half a tile an expert is not full).  In us, 128 against 64
+    // or 32: 4 experts of 500 rows, 2048 -> 2 x 2048, 48 / 40; 16 of 200, 3968 -> 72,
+    // 40 / 20; one of 2000, 4096 -> 4096, 88 / 76; but 16 of 1392, 3968 -> 72, 48 / 55.
+    const int64_t columns = ceil_div(c.N, kSilu ? kTileWeights / 2 : kTileWeights);
+    int tile_rows = kTileRows;
+    while (tile_rows > 32 && (c.num_rows / (tile_rows / 2) + (c.num_rows < c.E ? c.num_rows : c.E) / 2) * columns <= 320)
+        tile_rows /= 2;
+    const int64_t items = most_tiles(c, tile_rows) * columns;
     hipLaunchKernelGGL((tile_w4_kernel<kSilu>), dim3(blocks_for(items, 256)), dim3(kTileThreads), table_bytes(c.E),
                        c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows, c.capacity, c.codes,
-                       c.scales, c.E, c.K, c.N, above, static_cast<uint16_t*>(c.y));
+                       c.scales, c.E, c.K, c.N, above, tile_rows, static_cast<uint16_t*>(c.y));
     return hipGetLastError();
 }
 
