@@ -1,0 +1,64 @@
+"""ep_expert_linear_w4 in each of the ways the library takes (by rows of an
+expert, inputs, outputs and items), with the bounds of test_gpu_expert_w4.py."""
+import numpy as np
+import pytest
+import torch
+
+from combine_get_dispatch_02_amd import ep
+from test_gpu_expert_w4 import DEV, check, inputs, weights
+
+pytestmark = pytest.mark.gpu
+
+
+# Scales through shared memory (K % 512 == 0, up to 8192), eight at a time, singly.
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("K", [512, 1024, 2560, 7168, 8192, 8704, 768, 1280, 640, 1152])
+def test_streamed_and_split(K, silu):
+    check([1, 0, 16, 3], K, 40, silu, seed=K)
+    check([2], K, 72, silu, seed=K)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("K,N", [(512, 1000), (1536, 136), (768, 1000), (384, 1000), (256, 1000)])
+def test_streamed_whole(K, N, silu):
+    """Items for every wave: 90 experts of few rows."""
+    rng = np.random.default_rng(K)
+    check([int(v) for v in rng.integers(0, 16, 90)], K, N if N < 500 else N // (2 if silu else 1) // 8 * 8, silu, seed=K)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 1024, 1408])
+@pytest.mark.parametrize("rows", [17, 32, 33, 64, 65, 96, 97, 128, 129, 200])
+def test_tiles_of_every_height(rows, K, silu):
+    check([rows, 0, 40], K, 136, silu, seed=rows)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("N", [8, 56, 64, 72, 256, 264, 512, 520, 776])
+def test_tiles_of_every_width(N, silu):
+    check([70, 20], 256, N, silu, seed=N)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+def test_full_tiles(silu):
+    """So many rows and outputs that tiles keep their 128 rows."""
+    check([1601, 33, 0, 1570, 128, 2900], 256, 1032 if silu else 2056, silu, seed=1)
+
+
+@pytest.mark.parametrize("capacity,counts", [(33, [33, 16, 17, 0, 1]), (130, [130, 129, 16, 3, 64, 0]), (17, [17, 16, 0, 2])])
+def test_padded_regions_of_both_kinds(capacity, counts):
+    for silu in (False, True):
+        check(counts, 512, 88, silu, capacity=capacity, seed=capacity)
+
+
+def test_one_row_the_same_in_every_tile():
+    wc, ws = (torch.from_numpy(v).to(DEV) for v in weights(1, 600, 640, 2))
+    x = inputs(1, 640, 1).expand(1000, 640).contiguous().to(DEV)
+    y = ep.ep_expert_linear_w4(x, torch.tensor([0, 1000], dtype=torch.int32, device=DEV), wc, ws)
+    assert torch.equal(y, y[:1].expand_as(y))
+
+
+def test_skewed_batch_of_thousands():
+    """Zipf rows: one expert with most of them, many with one or none."""
+    counts = [int(v) for v in 3000 / np.arange(1, 200) ** 1.3]
+    check(counts + [0] * 57, 128, 40, True, seed=9)
