@@ -87,7 +87,7 @@ __device__ __forceinline__ Rows rows_of(const int32_t* __restrict__ expert_rows,
 // there only): the row tiles of every expert with more than `above` and at most
 // `most` rows, expert by expert, and for each the column tiles, which run
 // fastest.  In shared memory: start[e], the row tiles before expert e (at most
-// INT32_MAX: maps out of order could add up to more), start[E] in all.
+// INT32_MAX), start[E] in all.
 struct Table {
     int32_t* start;                                 // [E + 1]
     int32_t* first;                                 // [E] first row
@@ -103,40 +103,74 @@ __device__ __forceinline__ uint32_t add_limited(uint32_t a, uint32_t b) {
 __device__ Table make_table(int32_t* room, const int32_t* __restrict__ expert_rows, int E, int capacity,
                             int64_t num_rows, int tile_rows, int above, int most) {
     __shared__ uint32_t sums[8];
+    __shared__ uint64_t wrong[8];
     const Table t = {room, room + E + 1, room + 2 * E + 1};
     const int lane = lane_id(), wave = static_cast<int>(threadIdx.x) / kWave;
     const int threads = static_cast<int>(blockDim.x), per = (E + threads - 1) / threads;
     const int e0 = static_cast<int>(threadIdx.x) * per;
-    uint32_t mine = 0;
-    for (int i = 0; i < per; ++i) {
-        const int e = e0 + i;
-        if (e >= E) break;
-        const Rows r = rows_of(expert_rows, e, capacity, num_rows);
-        const int n = r.count > above && r.count <= most ? (r.count - 1) / tile_rows + 1 : 0;
-        t.start[e + 1] = n;                         // summed up below
-        t.first[e] = static_cast<int32_t>(r.first);
-        t.count[e] = r.count;
-        mine = add_limited(mine, n);
-    }
-    uint32_t upto = mine;
+    for (int pass = 0;; ++pass) {
+        uint32_t mine = 0;
+        bool bad = false;                           // offsets out of order or range
+        for (int i = 0; i < per; ++i) {
+            const int e = e0 + i;
+            if (e >= E) break;
+            if (pass == 0) {
+                const Rows r = rows_of(expert_rows, e, capacity, num_rows);
+                t.first[e] = static_cast<int32_t>(r.first);
+                t.count[e] = r.count;
+                bad |= capacity == 0 && (r.first != expert_rows[e] || r.first + r.count != expert_rows[e + 1]);
+            }
+            const int count = t.count[e], n = count > above && count <= most ? (count - 1) / tile_rows + 1 : 0;
+            t.start[e + 1] = n;                     // summed up below
+            mine = add_limited(mine, n);
+        }
+        uint32_t upto = mine;
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const uint32_t o = __shfl_up(upto, d);
-        if (lane >= d) upto = add_limited(upto, o);
+        for (int d = 1; d < kWave; d <<= 1) {
+            const uint32_t o = __shfl_up(upto, d);
+            if (lane >= d) upto = add_limited(upto, o);
+        }
+        const uint64_t any = ballot(bad);
+        if (lane == kWave - 1) {
+            sums[wave] = upto;
+            wrong[wave] = any;
+        }
+        uint32_t before = __shfl_up(upto, 1);
+        if (lane == 0) before = 0;
+        __syncthreads();
+        uint64_t repair = 0;
+        for (int w = 0; w < threads / kWave; ++w) {
+            if (w < wave) before = add_limited(before, sums[w]);
+            repair |= wrong[w];
+        }
+        if (repair) {
+            // A map that no dispatch makes: in order, each expert takes what the
+            // ones before it have left, so that no row has two experts and the
+            // work stays that of num_rows rows.
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                int64_t at = 0;
+                for (int e = 0; e < E; ++e) {
+                    const Rows r = rows_of(expert_rows, e, capacity, num_rows);
+                    const int64_t end = r.first + r.count;
+                    at = r.first > at ? r.first : at;
+                    t.first[e] = static_cast<int32_t>(at);
+                    t.count[e] = static_cast<int32_t>(end > at ? end - at : 0);
+                    at = end > at ? end : at;
+                }
+            }
+            __syncthreads();
+            continue;
+        }
+        if (threadIdx.x == 0) t.start[0] = 0;
+        for (int i = 0; i < per; ++i) {
+            if (e0 + i >= E) break;
+            before = add_limited(before, t.start[e0 + i + 1]);
+            t.start[e0 + i + 1] = before;
+        }
+        __syncthreads();
+        return t;
     }
-    if (lane == kWave - 1) sums[wave] = upto;
-    uint32_t before = __shfl_up(upto, 1);
-    if (lane == 0) before = 0;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) before = add_limited(before, sums[w]);
-    if (threadIdx.x == 0) t.start[0] = 0;
-    for (int i = 0; i < per; ++i) {
-        if (e0 + i >= E) break;
-        before = add_limited(before, t.start[e0 + i + 1]);
-        t.start[e0 + i + 1] = before;
-    }
-    __syncthreads();
-    return t;
 }
 
 // The expert whose row tiles include number `tile` < start[E]: every lane asks

@@ -399,7 +399,8 @@ int ep_route_backward(const void* logits, int logits_type, const int64_t* topk_i
  *   grad_topk_weights[t, j] = sum over h of g[h] * expert_out[r, h], in fp32
  * and grad_topk_weights[t, j] = 0 for every other slot.  Rows that no slot
  * maps to are not written.  Rows have to be distinct, as every dispatch makes
- * them: a row that two slots name gets the product of one of them.
+ * them: what is written to a row of grad_expert_out that two slots name is
+ * unspecified (grad_topk_weights is as above).
  * (The gradient of ep_dispatch with respect to x is ep_combine over the same
  * token_row with topk_weights NULL.)
  *
@@ -432,8 +433,10 @@ int ep_combine_backward(const void* grad_out, const void* expert_out, int64_t nu
  * capacity > 0: the padded layout of ep_dispatch_ll, expert_rows being
  * recv_count [E] (rows e*capacity .. e*capacity + expert_rows[e] - 1) and
  * num_rows = E*capacity.  Offsets are limited to [0, num_rows] and counts to
- * [0, capacity], so no map can make the kernel touch rows outside x and y;
- * rows of no expert are neither read for a result nor written.
+ * [0, capacity], and of offsets out of order an expert takes only rows that no
+ * expert before it has, so no map can make the kernel touch rows outside x and
+ * y or do more than num_rows rows' work.  Rows of no expert are neither read
+ * for a result nor written.
  *
  * Epilogue.  EP_EPILOGUE_NONE: W has out_features rows.
  * EP_EPILOGUE_SILU_MUL: W has 2*out_features rows, first the gate's, then the

@@ -62,3 +62,38 @@ def test_skewed_batch_of_thousands():
     """Zipf rows: one expert with most of them, many with one or none."""
     counts = [int(v) for v in 3000 / np.arange(1, 200) ** 1.3]
     check(counts + [0] * 57, 128, 40, True, seed=9)
+
+
+def test_offsets_out_of_order_share_no_row():
+    """Each expert takes what the ones before it have left."""
+    x = inputs(50, 256, 3)
+    wc, ws = weights(5, 24, 256, 4)
+    dev = [torch.from_numpy(v).to(DEV) for v in (wc, ws)]
+    for m, spans in (([0, 30, 10, 40, 20, 50], [(0, 30), (0, 0), (30, 10), (0, 0), (40, 10)]),
+                     ([-7, 20, 2 ** 31 - 1, 0, 50, 50], [(0, 20), (20, 30), (0, 0), (0, 0), (0, 0)]),
+                     ([40, 30, 20, 10, 5, 0], [(0, 0)] * 5),
+                     ([5, 5, 60, 60, 3, 2], [(0, 0), (5, 45), (0, 0), (0, 0), (0, 0)])):
+        y = torch.full((50, 24), 7.0, dtype=torch.bfloat16, device=DEV)
+        ep.ep_expert_linear_w4(x.to(DEV), torch.tensor(m, dtype=torch.int32, device=DEV), *dev, out=y)
+        ref = torch.full((50, 24), 7.0, dtype=torch.bfloat16, device=DEV)
+        for e, (first, count) in enumerate(spans):
+            if count:
+                off = torch.zeros(6, dtype=torch.int32, device=DEV)
+                off[e + 1:] = count
+                ref[first:first + count] = ep.ep_expert_linear_w4(x[first:first + count].to(DEV).contiguous(), off, *dev)
+        # One row alone may be split among waves where a batch is not.
+        assert torch.allclose(y.float(), ref.float(), rtol=2.0 ** -7, atol=1e-3)
+
+
+def test_scales_at_any_word():
+    """w_scales needs 4-byte alignment only."""
+    for K in (512, 1024, 768, 640):
+        wc, ws = weights(3, 48, K, 5)
+        room = torch.zeros(ws.size + 12, dtype=torch.uint8, device=DEV)
+        x, off = inputs(40, K, 1).to(DEV), torch.tensor([0, 3, 30, 40], dtype=torch.int32, device=DEV)
+        codes, scales = torch.from_numpy(wc).to(DEV), torch.from_numpy(ws).to(DEV)
+        ref = ep.ep_expert_linear_w4(x, off, codes, scales, epilogue="silu_mul")
+        for shift in (4, 8, 12):
+            room[shift:shift + ws.size] = scales.view(-1)
+            at = room[shift:shift + ws.size].view(3, 48, K // 32)
+            assert torch.equal(ep.ep_expert_linear_w4(x, off, codes, at, epilogue="silu_mul"), ref)
