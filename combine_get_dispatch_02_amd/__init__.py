@@ -1,4 +1,5 @@
-"""MI355X-native MoE expert-parallel dispatch / combine.
+"""MI355X-native MoE expert-parallel dispatch / combine, with the routing, the
+4-bit expert products and the gradients around them.
 
 The computation lives in libep.so (hand-written gfx950 HIP kernels behind the
 C ABI of include/ep.h).  This package holds its thin Python binding

@@ -5,7 +5,7 @@
 // token's g once and writes its row of dy; the dot product's order is fixed by
 // the launch shape, so results do not change from run to run.
 #include "ep_device.h"
-#include "ep_launch.h"
+#include "moe_launch.h"
 
 namespace ep {
 namespace {

@@ -12,6 +12,7 @@
 
 #include "../../include/ep.h"
 #include "ep_launch.h"
+#include "moe_launch.h"
 
 namespace {
 

@@ -12,7 +12,7 @@
 // groups of a 128-input block, and step s of four contracts inputs
 // 32 q + 8 s .. + 7 of every group q.
 #include "ep_device.h"
-#include "ep_launch.h"
+#include "moe_launch.h"
 
 namespace ep {
 namespace {

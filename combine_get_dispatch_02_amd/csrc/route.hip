@@ -12,7 +12,7 @@
 // about 80 instructions a token where repeated scans took 600.
 #include "../../include/ep.h"
 #include "ep_device.h"
-#include "ep_launch.h"
+#include "moe_launch.h"
 
 namespace ep {
 namespace {

@@ -10,7 +10,9 @@
  *   - the low-latency dispatch with per-token FP8 casting and one scale per
  *     128 channels (low-latency port commit, dispatch<kUseFP8,...>),
  *   - combine consuming the receiver-side layout produced by dispatch (commit
- *     fixing internode HT combine: receiver-side prefix sums).
+ *     fixing internode HT combine: receiver-side prefix sums),
+ * and, around that path, routing, the experts' products with 4-bit weights and
+ * the gradients of routing and combine.
  * On one GPU every destination "rank" is a contiguous range of one receive
  * buffer in this GPU's HBM: experts are split into num_ranks contiguous
  * blocks of num_experts/num_ranks, and rank r's rows are
