@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256) void combine_backward_short_kernel(
     for (int64_t s = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes; s < slots; s += step) {
         const int row = token_row[s];
         const bool valid = row >= 0 && row < num_rows;
-        float sum = 0.0f;
+        float sum = 0.0f, odd = 0.0f;
         if (valid && v < V) {
             const u32x4 a = g[s / k * V + v];
             const int64_t at = static_cast<int64_t>(row) * V + v;
@@ -107,8 +107,9 @@ __global__ __launch_bounds__(256) void combine_backward_short_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     sum = __builtin_fmaf(bf16_lo(a[i]), bf16_lo(b[i]), sum);
-                    sum = __builtin_fmaf(bf16_hi(a[i]), bf16_hi(b[i]), sum);
+                    odd = __builtin_fmaf(bf16_hi(a[i]), bf16_hi(b[i]), odd);
                 }
+                sum += odd;
             }
             if (kWithG) {
                 const float w = topk_weights ? topk_weights[s] : 1.0f;

@@ -1,6 +1,7 @@
 """ep_combine_backward on short rows (several slots a wave), with the bounds of
-test_gpu_combine_backward.py: a lane adds 8 products, the lanes join in at most 5
-steps, within the 11 roundings that the bound allows."""
+test_gpu_combine_backward.py: a lane adds 4 products to each of two sums (3
+roundings, for a product of bf16 numbers is exact), joins them (1) and its slot's
+lanes (at most 5): 9 of the 11 roundings that the bound allows."""
 import pytest
 
 from test_gpu_combine_backward import check, make

@@ -4,7 +4,10 @@ Experts are compared exactly.  Weights: a unit u is 2^-24, half a step of fp32.
 A score's exponent l - top is off by one unit of its size, its exp by 2 units
 (one step), the sum of up to 64 terms a lane and 6 joins by at most 70, the
 division and the scale by 2: with |l - top| <= span on both sides of the
-division, (2 span + 80) u in all.  Gradients: the same for each share and
+division, (2 span + 80) u in all.  (The sum over all experts uses the hardware's
+2^x, off by 2.5 units of l - top: 2.5 times the softmax's mean of |l - top|, which
+is at most ln 2048 = 7.6, so 19 of the 70, of which the sum itself has 38.)
+Gradients: the same for each share and
 score, a few units for the products, so (4 span + 240) u of the sum of the
 terms' magnitudes, then half a step of the logits' type.
 """

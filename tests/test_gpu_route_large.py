@@ -46,7 +46,7 @@ def test_sampled_tokens(T, E, k, dtype):
 
 
 @pytest.mark.parametrize("E,groups,topk_groups,k", [(256, 8, 4, 8), (128, 4, 1, 8), (64, 16, 5, 6), (160, 8, 3, 6), (256, 64, 9, 12),
-                                                    (96, 3, 2, 16), (32, 2, 1, 4)])
+                                                    (96, 3, 2, 16), (32, 2, 1, 4), (512, 8, 4, 8), (512, 4, 2, 12)])
 @pytest.mark.parametrize("group_top", [1, 2])
 def test_groups(E, groups, topk_groups, k, group_top):
     T = 4100
