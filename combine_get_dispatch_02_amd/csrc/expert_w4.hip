@@ -245,17 +245,18 @@ __device__ __forceinline__ uint32_t code_offset(const Operands& o, int n, int N,
 // The scales are a sixteenth of the codes' bytes, but 8 bytes of every row a step:
 // lines that the codes have driven out of the L1 by the next step.  An item's
 // scale rows lie together in memory, so they come into shared memory once, in
-// whole loads, where K <= kSharedScales and K % 512 == 0; else each step loads
-// eight of a row (K % 256 == 0) or single ones.  (128 experts of one row, 7168 ->
-// 2 x 2048, 2.0 GB: 345 us, 5.8 TB/s, against 432 with eight a load; 256 experts of
-// 4 rows, 2048 -> 7168, 2.0 GB: 406 against 446, of 16 rows 525 against 545.)
+// whole loads, where K <= kSharedScales; else each step loads eight of a row
+// (K % 256 == 0) or single ones.  (128 experts of one row, 7168 -> 2 x 2048, 2.0
+// GB: 345 us, 5.8 TB/s, against 432 with eight a load; 256 experts of 4 rows, 2048
+// -> 7168, 2.0 GB: 406 against 446; 60 experts of 2 rows, 5760 -> 2 x 1440: 113
+// against 150 with single ones.)
 enum Scales { kSingle, kEight, kShared };
 constexpr int kSharedScales = 8192;
 
 // 16-byte places of an item's block of scale rows, in whole loads of 64.
 template <bool kSilu>
 __device__ __forceinline__ int scale_slots(int K) {
-    return ((kSilu ? 32 : 64) * (K / 512) + 63) / 64 * 64;
+    return ((kSilu ? 32 : 64) * K / 512 + 63) / 64 * 64;
 }
 
 // Register s of the lanes of group q (lane / 16) and register q of group s change
@@ -290,8 +291,8 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
     // for all that is on the way.
     auto load = [&](int buf, int at) {
         at = at < K ? at : K - 128;
-        const int more = kScales != kSingle || at + 128 < K ? 128 : 0;
-        if (kScales != kSingle && at + 128 >= K) at = K - 256;
+        if (kScales == kEight && at + 128 >= K) at = K - 256;
+        const int more = kScales == kEight || at + 128 < K ? 128 : 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const Buffer wb = o.wb[kSilu ? j / 2 : 0], sb = o.sb[kSilu ? j / 2 : 0];
@@ -336,7 +337,8 @@ __device__ __forceinline__ void stream_products(const Operands& o, int k, int st
             for (int j = 0; j < 4; ++j) {
                 const int up = kSilu && j >= 2 ? scale_slots<kSilu>(K) * 16 : 0;
                 const int n = (kSilu ? j % 2 : j) * 16 + i16;
-                b[buf][j] = *reinterpret_cast<const u32x2*>(scale_rows + up + n * (K / 32) + here / 32);
+                const uint32_t* four = reinterpret_cast<const uint32_t*>(scale_rows + up + n * (K / 32) + here / 32);
+                b[buf][j] = u32x2{four[0], four[1]};    // the second four past the inputs' end are not used
             }
         }
         if (at < K) multiply(buf, 0);
@@ -408,12 +410,13 @@ __global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
         const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
         const Operands o = operands<kSilu>(x, codes, scales, e, row0, left, column * kOut, K, N);
         if (kScales == kShared) {
-            // Scale rows of 16 P bytes, P = K / 512, one after the other in memory
-            // as here: one block of 64 rows, or two of 32 (kSilu).  Past a block's
-            // or the outputs' last row its last bytes again.  (The wave's, or
+            // Scale rows of K / 32 bytes, one after the other in memory as here:
+            // one block of 64 rows, or two of 32 (kSilu), of whole pieces of 16
+            // bytes (K % 128 == 0, N % 8 == 0).  Past a block's or the outputs'
+            // last row its last bytes again.  (The wave's, or
             // behind the barriers below the block's, reads of the item before
             // are done.)
-            const int slots = scale_slots<kSilu>(K), last = (N - o.n0 < kOut ? N - o.n0 : kOut) * (K / 512) - 1;
+            const int slots = scale_slots<kSilu>(K), last = (N - o.n0 < kOut ? N - o.n0 : kOut) * (K / 128) / 4 - 1;
             for (int g = split ? wave : 0; g * 64 < slots * (kSilu ? 2 : 1); g += split ? 4 : 1) {
                 const bool up = kSilu && g * 64 >= slots;
                 const int at = g * 64 + lane - (up ? slots : 0);
@@ -688,7 +691,7 @@ hipError_t launch_stream(const Call& c, int most) {
 }
 template <bool kSilu>
 hipError_t launch_stream(const Call& c, int most) {
-    if (c.K % 512 == 0 && c.K <= kSharedScales) return launch_stream<kSilu, kShared>(c, most);
+    if (c.K <= kSharedScales) return launch_stream<kSilu, kShared>(c, most);
     return c.K % 256 == 0 ? launch_stream<kSilu, kEight>(c, most) : launch_stream<kSilu, kSingle>(c, most);
 }
 
