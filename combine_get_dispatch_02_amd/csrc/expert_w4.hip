@@ -509,35 +509,69 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
         const int r = (wave * kFill + i) * 4 + lane / 16;
         fill[i] = __umul24(r < o.left ? r : o.left - 1, K * 2) + place_of(r, lane % 16) * 16;
     }
-    u32x4 w[2][2][2];                           // [buffer][weight tile][u]
-    uint32_t b[2][2];                           // the four scales of 128 inputs
-    // Load number g of the six of a step's weights, and of its token rows.
+    // With few token rows the loads of the weights are the bound: a line of 128
+    // bytes is asked for at once, that is two steps' codes of a weight row, two
+    // steps ahead (a load for each step finds half of them gone from the L1), and
+    // the scales of four steps in one load.  256 experts of 32 rows, 7168 -> 2 x
+    // 2048, 4.0 GB: 888 us; a step's codes and scales one step ahead 1310; whole
+    // lines, their loads spread over the step 1092; whole lines and single steps'
+    // scales 1077.  64 experts of 24 rows, 4096 -> 2 x 1024: 75, 98, 87, 87.
+    // (Full tiles are bound by the matrix unit, and have no registers left.)
+    constexpr bool kLines = kTiles < 4;
+    constexpr int kBuffers = kLines ? 4 : 2;
+    u32x4 w[kBuffers][2][2];                    // [buffer][weight tile][u]
+    u32x4 b[2], later[2];                       // kLines: the scales of four steps, and the next four's
+    uint32_t b1[2][2];                          // else of one: [buffer][weight tile]
+    // Past the end the last step is asked for again.
+    auto within = [&](int kb) { return kb < K ? kb : K - 128; };
+    auto one_scale = [&](int j, int kb) { return load4(o.sb[kSilu ? j : 0], cr[j] / 16 - h, kb / 32); };
+    // Four steps' from kb on.  Where a row has fewer left, its last four (past the
+    // end of the last row nothing may be read), which from_last moves into place.
+    auto four_scales = [&](int j, int kb) {
+        return load16(o.sb[kSilu ? j : 0], cr[j] / 16 - h, (kb <= K - 512 ? kb : K - 512) / 32);
+    };
+    auto from_last = [&](u32x4 v, int kb) {
+        const int by = (kb - (K - 512)) / 128;
+        const bool one = by > 0 && by & 1, two = by > 0 && by & 2;
+        v = u32x4{one ? v[1] : v[0], one ? v[2] : v[1], one ? v[3] : v[2], v[3]};
+        return u32x4{two ? v[2] : v[0], two ? v[3] : v[1], v[2], v[3]};
+    };
+    // Load number g of the six of a step's weights.
     auto ask_weights = [&](int g, int buf, int kb) {
         const int j = g / 3, u = g % 3;
-        if (u == 2) b[buf][j] = load4(o.sb[kSilu ? j : 0], cr[j] / 16 - h, kb / 32);
+        if (u == 2) b1[buf][j] = one_scale(j, kb);
         else w[buf][j][u] = load16(o.wb[kSilu ? j : 0], cr[j], kb / 2 + 32 * u);
     };
+    // The four loads of a weight tile's codes for the steps at kb and kb + 128.
+    auto ask_lines = [&](int j, int buf, int kb) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            w[(buf + g / 2) % kBuffers][j][g % 2] =
+                load16(o.wb[kSilu ? j : 0], cr[j], within(kb + g / 2 * 128) / 2 + 32 * (g % 2));
+    };
+    // Load number g of a step's token rows.
     auto ask_rows = [&](int g, u32x4* to, int kb) {
         load_shared(to + (wave * kFill + g) * 64, o.xb, fill[g], kb * 2);
     };
-    // Past the end the last step is asked for again.
-    auto within = [&](int kb) { return kb < K ? kb : K - 128; };
     // Waves past the last output bring token rows only.
     const bool idle = o.n0 + wave * (kSilu ? 32 : 64) >= N;
     f32x16 acc[kTiles][2] = {};
-    bf16x8 v[kTiles], a[2];
+    // Registers for the inputs of two groups of products where there are enough.
+    constexpr int kReads = kTiles <= 2 ? 2 : 1;
+    bf16x8 v[kReads][kTiles], a[2];
     auto read = [&](const u32x4* from, int first, int i, int us) {
-        v[i] = __builtin_bit_cast(bf16x8, from[i * 512 + (first ^ ((us & 4) * 2 + us % 4))]);
+        v[us % kReads][i] = __builtin_bit_cast(bf16x8, from[i * 512 + (first ^ ((us & 4) * 2 + us % 4))]);
     };
     auto decode_tile = [&](int buf, int j, int us) {
-        const uint32_t scale = (b[buf][j] >> (8 * h + 16 * (us / 4)) & 0xFF) << 23;
+        const uint32_t scale = ((kLines ? b[j][buf] : b1[buf % 2][j]) >> (8 * h + 16 * (us / 4)) & 0xFF) << 23;
         return decode(w[buf][j][us / 4][us % 4], __uint_as_float(scale));
     };
     // The products of the step at kb, in 16 groups.  Between the groups its
     // loads are asked for, one at a time (all at once they hold up the
-    // wave's products): first the weights of the next step, and in the
-    // second half the token rows of the third next.  The barrier in the
-    // middle says that the next step's rows, asked for two steps ago, are in
+    // wave's products): first the weights of the next step (kLines: at every
+    // other step a weight tile's codes of the second and third next together),
+    // and in the second half the token rows of the third next.  The barrier in
+    // the middle says that the next step's rows, asked for two steps ago, are in
     // (behind them are at most one step's rows and weights: the vmcnt), and
     // that every wave is past the step before, whose rows are overwritten.
     // So no wave waits for memory at a barrier.  Each weight tile is decoded
@@ -562,19 +596,32 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
             for (int j = 0; j < 2; ++j) {
                 const int group = us * 2 + j;
                 __builtin_amdgcn_sched_barrier(0);
-                if (group < 6) ask_weights(group, 1 - buf, within(kb + 128));
-                if (group == 8) arrive<6 + kFill>();
+                if (!kLines && group < 6) ask_weights(group, 1 - buf, within(kb + 128));
+                if (kLines && buf % 2 == 0 && group % 4 == 0 && group < 8)
+                    ask_lines(group / 4, (buf + 2) % kBuffers, kb + 256);
+                if (kLines && buf == 3 && group < 2) later[group] = four_scales(group, kb + 128);
+                if (group == 8) {
+                    if (!kLines) arrive<6 + kFill>();
+                    else if (buf < 3) arrive<8 + kFill>();
+                    else arrive<10 + kFill>();
+                }
                 if (group > 8 && group - 9 < kFill) ask_rows(group - 9, to, within(kb + 384));
                 __builtin_amdgcn_sched_barrier(0);
                 if (j == 0) a[1] = decode_tile(buf, 1, us);
                 else if (us < 7) a[0] = decode_tile(buf, 0, us + 1);
-                else a[0] = decode_tile(1 - buf, 0, 0);
+                else {
+                    if (kLines && buf == 3) {
+                        b[0] = from_last(later[0], kb + 128);
+                        b[1] = from_last(later[1], kb + 128);
+                    }
+                    a[0] = decode_tile((buf + 1) % kBuffers, 0, 0);
+                }
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[j], v[i], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[j], v[us % kReads][i], acc[i][j], 0, 0, 0);
                     if (j == 1) {
-                        if (us < 7) read(from, first, i, us + 1);
-                        else read(then, first, i, 0);
+                        if (us + kReads < 8) read(from, first, i, us + kReads);
+                        else read(then, first, i, us + kReads - 8);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
@@ -583,8 +630,15 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     static_assert(kFill <= 7, "rows are asked for in the last seven groups");
     arrive<0>();                                // the last item's loads and reads are done
     if (!idle) {
+        if (kLines) {
+            ask_lines(0, 0, 0);
+            ask_lines(1, 0, 0);
+            b[0] = four_scales(0, 0);
+            b[1] = four_scales(1, 0);
+        } else {
 #pragma unroll
-        for (int g = 0; g < 6; ++g) ask_weights(g, 0, 0);
+            for (int g = 0; g < 6; ++g) ask_weights(g, 0, 0);
+        }
     }
 #pragma unroll
     for (int g = 0; g < kFill; ++g) ask_rows(g, s0, 0);
@@ -596,18 +650,20 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     if (!idle) {
         a[0] = decode_tile(0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) read(s0, i32 * 16 + place_of(i32, 4 * h), i, 0);
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int us = 0; us < kReads; ++us) read(s0, i32 * 16 + place_of(i32, 4 * h), i, us);
     }
     int kb = 0;
     for (; kb + 512 <= K; kb += 512) {
         multiply(s0, s1, s3, 0, kb);
         multiply(s1, s2, s0, 1, kb + 128);
-        multiply(s2, s3, s1, 0, kb + 256);
-        multiply(s3, s0, s2, 1, kb + 384);
+        multiply(s2, s3, s1, 2 % kBuffers, kb + 256);
+        multiply(s3, s0, s2, 3 % kBuffers, kb + 384);
     }
     if (kb < K) multiply(s0, s1, s3, 0, kb);
     if (kb + 128 < K) multiply(s1, s2, s0, 1, kb + 128);
-    if (kb + 256 < K) multiply(s2, s3, s1, 0, kb + 256);
+    if (kb + 256 < K) multiply(s2, s3, s1, 2 % kBuffers, kb + 256);
 
     // A lane holds outputs 8 p + 4 h .. + 3 (p = 0 .. 3) of token row i32 of
     // each 32 x 32 tile.
@@ -652,8 +708,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_w4_kernel(
         const Operands o = operands<kSilu>(x, codes, scales, e, row0, left,
                                            static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut, K, N);
         // An expert's last tile is not full: products of rows that are not there
-        // would cost what the others do.
-        if (left > 96) tile_item<kSilu, 4>(o, K, N, y, s0, s1, s2, s3);
+        // would cost what the others do.  (The smaller ones load the scales of 512
+        // inputs at once.)
+        if (left > 96 || K < 512) tile_item<kSilu, 4>(o, K, N, y, s0, s1, s2, s3);
         else if (left > 64) tile_item<kSilu, 3>(o, K, N, y, s0, s1, s2, s3);
         else if (left > 32) tile_item<kSilu, 2>(o, K, N, y, s0, s1, s2, s3);
         else tile_item<kSilu, 1>(o, K, N, y, s0, s1, s2, s3);

@@ -10,9 +10,9 @@ from test_gpu_expert_w4 import DEV, check, inputs, weights
 pytestmark = pytest.mark.gpu
 
 
-# Scales through shared memory (K % 512 == 0, up to 8192), eight at a time, singly.
+# Scales through shared memory (K up to 8192), eight at a time (K % 256 == 0), singly.
 @pytest.mark.parametrize("silu", [False, True])
-@pytest.mark.parametrize("K", [512, 1024, 2560, 7168, 8192, 8704, 768, 1280, 640, 1152])
+@pytest.mark.parametrize("K", [128, 256, 512, 1024, 2560, 7168, 8064, 8192, 8320, 8704, 768, 1280, 640, 1152])
 def test_streamed_and_split(K, silu):
     check([1, 0, 16, 3], K, 40, silu, seed=K)
     check([2], K, 72, silu, seed=K)
@@ -31,6 +31,14 @@ def test_streamed_whole(K, N, silu):
 @pytest.mark.parametrize("rows", [17, 32, 33, 64, 65, 96, 97, 128, 129, 200])
 def test_tiles_of_every_height(rows, K, silu):
     check([rows, 0, 40], K, 136, silu, seed=rows)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("K", [768, 896, 1152, 1280, 2048, 2176])
+@pytest.mark.parametrize("rows", [20, 60, 90])
+def test_tiles_of_every_depth(rows, K, silu):
+    """Inputs that end 0 to 3 steps into the four whose scales are loaded at once."""
+    check([rows, 17], K, 1032, silu, seed=rows)
 
 
 @pytest.mark.parametrize("silu", [False, True])
