@@ -34,11 +34,14 @@ def test_tiles_of_every_height(rows, K, silu):
 
 
 @pytest.mark.parametrize("silu", [False, True])
-@pytest.mark.parametrize("K", [768, 896, 1152, 1280, 2048, 2176])
-@pytest.mark.parametrize("rows", [20, 60, 90])
-def test_tiles_of_every_depth(rows, K, silu):
-    """Inputs that end 0 to 3 steps into the four whose scales are loaded at once."""
-    check([rows, 17], K, 1032, silu, seed=rows)
+@pytest.mark.parametrize("K", [128, 384, 512, 640, 768, 896, 1152])
+@pytest.mark.parametrize("tallest", [64, 128])
+def test_tiles_of_every_height_and_depth(tallest, K, silu):
+    """36 experts and outputs enough for tiles of `tallest` rows, which are full,
+    or end after 1 to 4 times 32 rows; inputs that end 0 to 3 steps into the four
+    whose scales are loaded at once."""
+    counts = [int(v) for v in np.linspace(13, tallest, 36)]
+    check(counts, K, 1288 if silu else 2568, silu, seed=K)
 
 
 @pytest.mark.parametrize("silu", [False, True])
@@ -57,6 +60,15 @@ def test_full_tiles(silu):
 def test_padded_regions_of_both_kinds(capacity, counts):
     for silu in (False, True):
         check(counts, 512, 88, silu, capacity=capacity, seed=capacity)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("K", [256, 640, 1024])
+def test_rows_about_the_two_ways(K, silu):
+    counts = [12, 13, 0, 11, 16, 14, 12, 17, 1]
+    check(counts, K, 72, silu, seed=K)
+    check(counts, K, 72, silu, capacity=17, seed=K)
+    check([12, 3, 0, 11], K, 72, silu, capacity=12, seed=K)
 
 
 def test_one_row_the_same_in_every_tile():
