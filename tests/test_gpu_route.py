@@ -173,6 +173,20 @@ def test_backward_takes_any_ids(dtype, sigmoid, renorm):
     check_backward(l, idx, torch.randn(6, 5, generator=torch.Generator().manual_seed(4)), sigmoid, renorm, 0.7)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("T,E", [(5, 31), (4483, 31), (9000, 104), (40, 512)])
+def test_one_renormalised_choice_has_no_gradient(T, E, sigmoid, dtype):
+    """Its weight is the scale whatever the logits: a / a is 1 and g - g is 0, with
+    no rounding in between."""
+    l = (30 * make(T, E, dtype, 5).float()).to(TYPES[dtype]).to(DEV)
+    score = "sigmoid" if sigmoid else "softmax"
+    r = ep.ep_route(l, 1, score=score, renormalize=True, scale=2.5)
+    assert (r["topk_weights"] == 2.5).all()
+    g = torch.randn(T, 1, generator=torch.Generator().manual_seed(6)).to(DEV)
+    assert (ep.ep_route_backward(l, r["topk_idx"], g, score=score, renormalize=True, scale=2.5) == 0).all()
+
+
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_backward_against_differences(sigmoid, renorm):
