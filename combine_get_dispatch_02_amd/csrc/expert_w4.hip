@@ -13,6 +13,7 @@
 // 32 q + 8 s .. + 7 of every group q.
 #include "ep_device.h"
 #include "moe_launch.h"
+#include "w4_plan.h"
 
 namespace ep {
 namespace {
@@ -491,6 +492,17 @@ __device__ __forceinline__ void arrive() {
 // Shared memory serves 16 lanes at a time, of 16 different rows mod 16.
 __device__ __forceinline__ int place_of(int r, int c) { return c ^ (r & 15); }
 
+// arrive<later>() for the counts of tile_step.
+template <int kTiles>
+__device__ __forceinline__ void arrive_but(int later) {
+    if (later == 0) arrive<0>();
+    else if (later == kTiles) arrive<kTiles>();
+    else if (later == 6) arrive<6>();
+    else if (later == kTiles + 6) arrive<kTiles + 6>();
+    else if (later == kTiles + 8) arrive<kTiles + 8>();
+    else arrive<kTiles + 10>();
+}
+
 // One item: up to 32 kTiles token rows.
 template <bool kSilu, int kTiles>
 __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint16_t* __restrict__ y, u32x4* s0,
@@ -542,12 +554,13 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
         if (u == 2) b1[buf][j] = one_scale(j, kb);
         else w[buf][j][u] = load16(o.wb[kSilu ? j : 0], cr[j], kb / 2 + 32 * u);
     };
-    // The four loads of a weight tile's codes for the steps at kb and kb + 128.
-    auto ask_lines = [&](int j, int buf, int kb) {
+    // The loads of a weight tile's codes for the steps at kb and, of four, kb + 128.
+    auto ask_lines = [&](int j, int buf, int kb, int loads) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-            w[(buf + g / 2) % kBuffers][j][g % 2] =
-                load16(o.wb[kSilu ? j : 0], cr[j], within(kb + g / 2 * 128) / 2 + 32 * (g % 2));
+            if (g < loads)
+                w[(buf + g / 2) % kBuffers][j][g % 2] =
+                    load16(o.wb[kSilu ? j : 0], cr[j], within(kb + g / 2 * 128) / 2 + 32 * (g % 2));
     };
     // Load number g of a step's token rows.
     auto ask_rows = [&](int g, u32x4* to, int kb) {
@@ -577,12 +590,15 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     // So no wave waits for memory at a barrier.  Each weight tile is decoded
     // beside the products of the one before; the next inputs of a row tile
     // are read when its last product is under way.  The barriers to
-    // scheduling keep all that in place.
-    auto multiply = [&](const u32x4* from, const u32x4* then, u32x4* to, int buf, int kb) {
+    // scheduling keep all that in place.  rest: 0 in the loop, 1 .. 3 the steps
+    // after it; the loads and counts of each are tile_step's.
+    auto multiply = [&](const u32x4* from, const u32x4* then, u32x4* to, int buf, int rest, int kb) {
+        const TileStep step = tile_step(kTiles, buf, rest);     // constants where this is called
         if (idle) {
-            arrive<kFill>();                        // behind the next step's rows, one step's
+            arrive_but<kTiles>(step.idle_later);
 #pragma unroll
-            for (int g = 0; g < kFill; ++g) ask_rows(g, to, within(kb + 384));
+            for (int g = 0; g < kFill; ++g)
+                if (g < step.fills) ask_rows(g, to, within(kb + 384));
             return;
         }
         // Place 4 h of row i32, from which the others differ by an exclusive or:
@@ -596,21 +612,18 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
             for (int j = 0; j < 2; ++j) {
                 const int group = us * 2 + j;
                 __builtin_amdgcn_sched_barrier(0);
-                if (!kLines && group < 6) ask_weights(group, 1 - buf, within(kb + 128));
-                if (kLines && buf % 2 == 0 && group % 4 == 0 && group < 8)
-                    ask_lines(group / 4, (buf + 2) % kBuffers, kb + 256);
-                if (kLines && buf == 3 && group < 2) later[group] = four_scales(group, kb + 128);
-                if (group == 8) {
-                    if (!kLines) arrive<6 + kFill>();
-                    else if (buf < 3) arrive<8 + kFill>();
-                    else arrive<10 + kFill>();
-                }
-                if (group > 8 && group - 9 < kFill) ask_rows(group - 9, to, within(kb + 384));
+                if (!kLines && group < step.weights) ask_weights(group, 1 - buf, within(kb + 128));
+                // Of two weight tiles, before the barrier or behind it.
+                if (kLines && step.weights >= 4 && (group == (step.late ? 9 : 0) || group == (step.late ? 13 : 4)))
+                    ask_lines(group % 8 / 4, (buf + 2) % kBuffers, kb + 256, step.weights / 2);
+                if (kLines && step.weights == 2 && group < 2) later[group] = four_scales(group, kb + 128);
+                if (group == 8) arrive_but<kTiles>(step.later);
+                if (group > 8 && group - 9 < step.fills) ask_rows(group - 9, to, within(kb + 384));
                 __builtin_amdgcn_sched_barrier(0);
                 if (j == 0) a[1] = decode_tile(buf, 1, us);
                 else if (us < 7) a[0] = decode_tile(buf, 0, us + 1);
                 else {
-                    if (kLines && buf == 3) {
+                    if (kLines && step.weights == 2) {
                         b[0] = from_last(later[0], kb + 128);
                         b[1] = from_last(later[1], kb + 128);
                     }
@@ -631,8 +644,8 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     arrive<0>();                                // the last item's loads and reads are done
     if (!idle) {
         if (kLines) {
-            ask_lines(0, 0, 0);
-            ask_lines(1, 0, 0);
+            ask_lines(0, 0, 0, 4);
+            ask_lines(1, 0, 0, 4);
             b[0] = four_scales(0, 0);
             b[1] = four_scales(1, 0);
         } else {
@@ -656,14 +669,14 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     }
     int kb = 0;
     for (; kb + 512 <= K; kb += 512) {
-        multiply(s0, s1, s3, 0, kb);
-        multiply(s1, s2, s0, 1, kb + 128);
-        multiply(s2, s3, s1, 2 % kBuffers, kb + 256);
-        multiply(s3, s0, s2, 3 % kBuffers, kb + 384);
+        multiply(s0, s1, s3, 0, 0, kb);
+        multiply(s1, s2, s0, 1, 0, kb + 128);
+        multiply(s2, s3, s1, 2 % kBuffers, 0, kb + 256);
+        multiply(s3, s0, s2, 3 % kBuffers, 0, kb + 384);
     }
-    if (kb < K) multiply(s0, s1, s3, 0, kb);
-    if (kb + 128 < K) multiply(s1, s2, s0, 1, kb + 128);
-    if (kb + 256 < K) multiply(s2, s3, s1, 2 % kBuffers, kb + 256);
+    if (kb < K) multiply(s0, s1, s3, 0, 1, kb);
+    if (kb + 128 < K) multiply(s1, s2, s0, 1, 2, kb + 128);
+    if (kb + 256 < K) multiply(s2, s3, s1, 2 % kBuffers, 3, kb + 256);
 
     // A lane holds outputs 8 p + 4 h .. + 3 (p = 0 .. 3) of token row i32 of
     // each 32 x 32 tile.
