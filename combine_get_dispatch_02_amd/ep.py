@@ -530,6 +530,19 @@ _SCORES = {"softmax": 0, "sigmoid": 1}                                  # EP_SCO
 _EPILOGUES = {"none": 0, "silu_mul": 1}                                 # EP_EPILOGUE_*
 
 
+def _need_int32(fn: str, **values: int) -> None:
+    """ctypes passes the low 32 bits of a larger number on without a word.  (Called
+    where the sign or a bit past the 31st shows in the values or-ed together: small
+    calls pay for one shift.)"""
+    for name, v in values.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{fn}: {name} = {v} does not fit a 32-bit argument")
+
+
+def _last(shape: torch.Size) -> int:
+    return shape[-1] if shape else 0
+
+
 def _need_logits(logits: torch.Tensor, score: str) -> None:
     if logits.dtype not in _TYPES:
         raise TypeError(f"logits must be one of {', '.join(map(str, _TYPES))}, got {logits.dtype}")
@@ -551,14 +564,17 @@ def ep_route(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
     without the bias, renormalised over the chosen ones if `renormalize`,
     times `scale`.  Experts whose logit is -inf or NaN are never chosen; where
     fewer than k are left the slots are empty (-1, weight 0)."""
+    k, shape = int(num_topk), logits.shape
+    if (k | num_groups | topk_groups | group_top | _last(shape)) >> 31:
+        _need_int32("ep_route", num_topk=k, num_groups=num_groups, topk_groups=topk_groups, group_top=group_top,
+                    num_experts=_last(shape))
     _need_logits(logits, score)
     dev = logits.device
-    T, E = logits.shape
+    T, E = shape
     if bias is not None:
         _need(bias, "bias", torch.float32, dev)
         if tuple(bias.shape) != (E,):
             raise ValueError("bias must be [E]")
-    k = int(num_topk)
     if out is None:
         # A bad num_topk is the library's to refuse.
         out = dict(topk_idx=torch.empty((T, max(k, 0)), dtype=torch.int64, device=dev),
@@ -578,11 +594,14 @@ def ep_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights
     """Gradient of ep_route's topk_weights with respect to the logits: [T, E]
     in the logits' type, from grad_weights [T, k] fp32 and the topk_idx that
     ep_route chose.  score, renormalize and scale as in the forward call."""
+    shape = logits.shape
+    if (_last(shape) | _last(topk_idx.shape)) >> 31:
+        _need_int32("ep_route_backward", num_experts=_last(shape), num_topk=_last(topk_idx.shape))
     _need_logits(logits, score)
     dev = logits.device
     _need(topk_idx, "topk_idx", torch.int64, dev)
     _need(grad_weights, "grad_weights", torch.float32, dev)
-    T, E = logits.shape
+    T, E = shape
     if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
         raise ValueError("logits and topk_idx disagree on num_tokens")
     if grad_weights.shape != topk_idx.shape:
@@ -607,6 +626,8 @@ def ep_combine_backward(grad_out: torch.Tensor, expert_out: Optional[torch.Tenso
     of the two alone, and only that one is computed.  Rows have to be distinct,
     as every dispatch makes them.  The gradient of ep_dispatch is
     ep_combine(grad_recv_x, token_row, None)."""
+    if (_last(grad_out.shape) | _last(token_row.shape)) >> 31:
+        _need_int32("ep_combine_backward", hidden=_last(grad_out.shape), num_topk=_last(token_row.shape))
     _need(grad_out, "grad_out", torch.bfloat16)
     dev = grad_out.device
     _need(token_row, "token_row", torch.int32, dev)
@@ -654,6 +675,10 @@ def ep_expert_linear_w4(x: torch.Tensor, expert_rows: torch.Tensor, w_codes: tor
     epilogue "silu_mul": W = 2N, gate rows first, y = silu(gate) * up; "none":
     W = N.  Rows of no expert are left as they were (uninitialised unless
     `out` is given)."""
+    weights = w_codes.shape
+    if (capacity | _last(x.shape) | max(weights, default=0)) >> 31:
+        _need_int32("ep_expert_linear_w4", capacity=capacity, in_features=_last(x.shape),
+                    weights=max(weights, default=0))
     _need(x, "x", torch.bfloat16)
     dev = x.device
     _need(expert_rows, "expert_rows", torch.int32, dev)
