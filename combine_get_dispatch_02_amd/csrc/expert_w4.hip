@@ -24,7 +24,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
-constexpr int kTileRows = 128, kTileWeights = 512, kTileThreads = 512;
+constexpr int kTileThreads = 512;
 
 // Eight codes of one word, times the scale 2^(b - 127) whose bits are b << 23.
 __device__ __forceinline__ bf16x8 decode(uint32_t codes, float scale) {
@@ -251,8 +251,6 @@ __device__ __forceinline__ uint32_t code_offset(const Operands& o, int n, int N,
 // GB: 345 us, 5.8 TB/s, against 432 with eight a load; 256 experts of 4 rows, 2048
 // -> 7168, 2.0 GB: 406 against 446; 60 experts of 2 rows, 5760 -> 2 x 1440: 113
 // against 150 with single ones.)
-enum Scales { kSingle, kEight, kShared };
-constexpr int kSharedScales = 8192;
 
 // 16-byte places of an item's block of scale rows, in whole loads of 64.
 template <bool kSilu>
@@ -761,59 +759,31 @@ hipError_t launch_stream(const Call& c, int most) {
 }
 template <bool kSilu>
 hipError_t launch_stream(const Call& c, int most) {
-    if (c.K <= kSharedScales) return launch_stream<kSilu, kShared>(c, most);
-    return c.K % 256 == 0 ? launch_stream<kSilu, kEight>(c, most) : launch_stream<kSilu, kSingle>(c, most);
+    switch (w4_scales(c.K)) {
+        case kShared: return launch_stream<kSilu, kShared>(c, most);
+        case kEight: return launch_stream<kSilu, kEight>(c, most);
+        default: return launch_stream<kSilu, kSingle>(c, most);
+    }
 }
 
 template <bool kSilu>
-hipError_t launch_tile(const Call& c, int above) {
-    // Smaller tiles where they all run at once and those of 128 rows would leave
-    // CUs without one (half a tile an expert is not full).  In us, 128 against 64
-    // or 32: 4 experts of 500 rows, 2048 -> 2 x 2048, 45 / 37; 16 of 200, 3968 -> 72,
-    // 41 / 20; one of 2000, 4096 -> 4096, 80 / 67; 64 of 206, 5760 -> 504, 113 / 86;
-    // but 16 of 1392, 3968 -> 72, 48 / 54; 64 of 64, 4096 -> 2 x 1024, 86 / 112.
+hipError_t launch_tile(const Call& c, const W4Plan& plan) {
     const int64_t columns = ceil_div(c.N, kSilu ? kTileWeights / 2 : kTileWeights);
-    int tile_rows = kTileRows;
-    while (tile_rows > 32 && (c.num_rows / (tile_rows / 2) + (c.num_rows < c.E ? c.num_rows : c.E) / 2) * columns <= 320)
-        tile_rows /= 2;
-    const int64_t items = most_tiles(c, tile_rows) * columns;
+    const int64_t items = most_tiles(c, plan.tile_rows) * columns;
     hipLaunchKernelGGL((tile_w4_kernel<kSilu>), dim3(blocks_for(items, 256)), dim3(kTileThreads), table_bytes(c.E),
                        c.stream, static_cast<const uint16_t*>(c.x), c.num_rows, c.expert_rows, c.capacity, c.codes,
-                       c.scales, c.E, c.K, c.N, above, tile_rows, static_cast<uint16_t*>(c.y));
+                       c.scales, c.E, c.K, c.N, plan.tile_above, plan.tile_rows, static_cast<uint16_t*>(c.y));
     return hipGetLastError();
 }
 
-// Rows of an expert up to which its weights are streamed.  Streams against tiles
-// (us), of 4, 8, 12 and 16 rows: 64 experts, 4096 -> 2 x 1024, 61 / 70, 65 / 70,
-// 70 / 71, 75 / 71; 256 experts, 2048 -> 7168, 410 / 447, 460 / 453, 493 / 458,
-// 531 / 469; 256 experts, 7168 -> 2 x 2048, 697 / 840, 758 / 851, 843 / 868, 905 / 876;
-// 60 experts, 2048 -> 2 x 1408, 51 / 64, 54 / 64, 57 / 64, 62 / 64.
-constexpr int kFew = 12;
-
-// But where the streams' items (16 rows x 64 weight rows, half a tile an expert
-// not full) find room on the card at once, streams take all rows: tiles have an
-// eighth of the items, and leave CUs without one.  Streams against tiles (us), by
-// items: 60, 8 experts of 16 rows, 3968 -> 432, 15 / 31; 544, one of 128, 4096 ->
-// 4096, 26 / 49; 690, 60 of 17, 2048 -> 2 x 256, 22 / 32; 1152, 8 of 64, 7168 -> 2048,
-// 57 / 79; 1024, 64 of 24, 512 -> 512, 14.7 / 13.3; but 2048, 8 of 24, 3968 -> 8192,
-// 62 / 57; 2176, 8 of 128, 3968 -> 2048, 55 / 38.  Long experts with few outputs
-// read more token rows than weights: one of 4000, 1024 -> 72 (502 items) 17 / 10; 16
-// of 400, 3968 -> 72, 26 / 22; 16 of 200, 19 / 20.
-constexpr int64_t kAllItems = 1280, kAllMean = 256;
-
 template <bool kSilu>
 hipError_t launch(const Call& c) {
-    // The rows of an expert are known on the device only; each launch takes the
-    // experts that suit it, and one is left out where it would find none or few.
-    const int64_t most = c.capacity > 0 ? c.capacity : c.num_rows, mean = c.num_rows / c.E;
-    const int64_t tiles = c.num_rows / 16 + (c.num_rows < c.E ? c.num_rows : c.E) / 2;
-    if (mean <= kAllMean && tiles * ceil_div(c.N, kSilu ? 32 : 64) <= kAllItems) return launch_stream<kSilu>(c, INT32_MAX);
-    if (c.capacity > 0 || mean <= 2 * kFew) {
-        const hipError_t e = launch_stream<kSilu>(c, kFew);
-        if (e != hipSuccess || most <= kFew) return e;
-        return launch_tile<kSilu>(c, kFew);
+    const W4Plan plan = w4_plan(c.num_rows, c.capacity, c.E, c.N, kSilu);
+    if (plan.stream_most > 0) {
+        const hipError_t e = launch_stream<kSilu>(c, plan.stream_most);
+        if (e != hipSuccess) return e;
     }
-    return launch_tile<kSilu>(c, 0);
+    return plan.tile_above < INT32_MAX ? launch_tile<kSilu>(c, plan) : hipSuccess;
 }
 
 }  // namespace
