@@ -562,8 +562,9 @@ def ep_route(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
     plus `bias` [E], out of the topk_groups best of num_groups groups (a
     group's score is the sum of its group_top best); weights are the scores
     without the bias, renormalised over the chosen ones if `renormalize`,
-    times `scale`.  Experts whose logit is -inf or NaN are never chosen; where
-    fewer than k are left the slots are empty (-1, weight 0)."""
+    times `scale`.  Experts whose logit is -inf or NaN are never chosen and have
+    no part in a softmax; those whose bias is are never chosen, but keep theirs.
+    Where fewer than k are left the slots are empty (-1, weight 0)."""
     k, shape = int(num_topk), logits.shape
     if (k | num_groups | topk_groups | group_top | _last(shape)) >> 31:
         _need_int32("ep_route", num_topk=k, num_groups=num_groups, topk_groups=topk_groups, group_top=group_top,

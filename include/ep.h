@@ -335,7 +335,9 @@ int ep_combine(const void* expert_out, int64_t num_rows, const int32_t* token_ro
  *           group_top == 1 experts are ranked by the logits themselves: the
  *           order of the exact scores, free of their rounding.
  *   An expert whose logit or choice is -inf or NaN is unavailable: it is never
- *   chosen and its softmax term is 0.
+ *   chosen.  A logit of -inf or NaN also has a softmax term of 0.  A bias steers
+ *   the choice only: an expert that it makes unavailable keeps its score, which
+ *   counts in the sum over all E logits (mask the logit to leave it out).
  *   groups  num_groups contiguous blocks of E / num_groups experts.  A group's
  *           score is the fp32 sum of its group_top (1 or 2) largest available
  *           choices; only the experts of the topk_groups best groups stay.
