@@ -1,16 +1,16 @@
 // expert_w4.hip -- ep_expert_linear_w4 on gfx950.
 //
 // y[r] = x[r] . W[e(r)]^T over the rows of each expert, W in E2M1 codes with
-// one E8M0 scale per 32 inputs.  The matrix instruction contracts 32 inputs of
-// 16 weight rows against 16 token rows (v_mfma_f32_16x16x32_bf16).  A code
-// times its scale is exact in bf16, so the only roundings are the fp32
-// accumulation and the final one to bf16.
+// one E8M0 scale per 32 inputs.  A code times its scale is exact in bf16, so the
+// only roundings are the fp32 accumulation and the final one to bf16.
 //
 // The order of the contraction is free as long as both operands agree, so a
 // lane takes 16 consecutive bytes of its weight row: 32 inputs, exactly one
-// scale group.  The four lane groups of a wave (lane / 16) hold the four
-// groups of a 128-input block, and step s of four contracts inputs
-// 32 q + 8 s .. + 7 of every group q.
+// scale group.  Streams (few rows) contract 32 inputs of 16 weight rows against 16
+// token rows at a time (v_mfma_f32_16x16x32_bf16): the four lane groups of a wave
+// (lane / 16) hold the four scale groups of a 128-input block, and step s of four
+// contracts inputs 32 q + 8 s .. + 7 of every group q.  Tiles (many rows) take 16
+// inputs of 32 rows against 32 (v_mfma_f32_32x32x16_bf16), as written there.
 #include "ep_device.h"
 #include "moe_launch.h"
 #include "w4_plan.h"
@@ -464,11 +464,12 @@ __global__ __launch_bounds__(kThreads, 2) void stream_w4_kernel(
 }
 
 // ---- many rows per expert: bound by the matrix unit ------------------------------
-// One item: 32 kTiles token rows x 256 weight rows (kSilu: 128 gate rows and
-// their 128 up rows), 64 of them to each of the four waves, so that no code is
-// decoded twice.  The token rows of a 128-input step come through shared memory
-// (two buffers, loaded past the registers); the codes go straight into the
-// registers of the wave that decodes them.  Both are asked for a step ahead.
+// One item: 32 kTiles token rows x 512 weight rows (kSilu: 256 gate rows and
+// their 256 up rows), 64 of them to each of the block's eight waves, so that no code
+// is decoded twice.  The token rows of a 128-input step come through shared memory
+// (four buffers, loaded past the registers, asked for three steps ahead); the codes
+// go straight into the registers of the wave that decodes them, asked for a step
+// ahead or, with up to 96 rows, two steps' at a time.
 
 // Products are 32 x 32 here (v_mfma_f32_32x32x16_bf16): per operation they read
 // half the operand registers of the 16 x 16 form, and at these sizes the card's
@@ -520,8 +521,8 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
         fill[i] = __umul24(r < o.left ? r : o.left - 1, K * 2) + place_of(r, lane % 16) * 16;
     }
     // With few token rows the loads of the weights are the bound: a line of 128
-    // bytes is asked for at once, that is two steps' codes of a weight row, two
-    // steps ahead (a load for each step finds half of them gone from the L1), and
+    // bytes is asked for at once, that is two steps' codes of a weight row, two and
+    // three steps ahead (a load for each step finds half of them gone from the L1), and
     // the scales of four steps in one load.  256 experts of 32 rows, 7168 -> 2 x
     // 2048, 4.0 GB: 888 us; a step's codes and scales one step ahead 1310; whole
     // lines, their loads spread over the step 1092; whole lines and single steps'
@@ -585,7 +586,12 @@ __device__ __forceinline__ void tile_item(const Operands& o, int K, int N, uint1
     // the middle says that the next step's rows, asked for two steps ago, are in
     // (behind them are at most one step's rows and weights: the vmcnt), and
     // that every wave is past the step before, whose rows are overwritten.
-    // So no wave waits for memory at a barrier.  Each weight tile is decoded
+    // By these counts no wave would wait for what it needs two steps later; but
+    // the compiler takes a read of any of the four buffers for one of what the
+    // loads past the registers are still writing, and puts waits of its own before
+    // reads: for the rows asked for half a step ago in full tiles, and for all of the
+    // codes asked for a step ago in the others.  (They are not needed: the barrier
+    // is the wait.)  Each weight tile is decoded
     // beside the products of the one before; the next inputs of a row tile
     // are read when its last product is under way.  The barriers to
     // scheduling keep all that in place.  rest: 0 in the loop, 1 .. 3 the steps

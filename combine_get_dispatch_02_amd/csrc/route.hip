@@ -4,12 +4,15 @@
 // the gradient back.
 //
 // Choosing.  L lanes of a wave hold one token (64 / L tokens a wave), C of its
-// experts each.  A choice and its expert make one 64-bit key that is also a positive double, so that one
-// instruction (v_max_f64, as fast as an fp32 one here) compares both, ties
-// included.  Every lane sorts its keys once (a network of v_max / v_min); each of
-// the k rounds is then a maximum over the lanes' first keys, and the lane that
-// had it moves up its list.  For 32768 tokens of 256 experts, top 8, that is
-// about 80 instructions a token where repeated scans took 600.
+// experts each.  A choice and its expert make one 64-bit key that is also a positive
+// double, so that one instruction (v_max_f64, as fast as an fp32 one here) compares
+// both, ties included.  Every lane sorts its keys once (a network of v_max / v_min);
+// each of the k rounds is then a maximum over the lanes' first keys, and the lane
+// that had it moves up its list.  For 32768 tokens of 256 experts, top 8, by logits,
+// that is about 780 vector instructions a wave of four tokens, 530 of them the sort
+// and the rounds.  Another 400 before the loop over tokens, most of them the group
+// code's, which the compiler takes out of the loop whether there are groups or not,
+// are paid by every wave, as the grid has a wave for every four tokens.
 #include "../../include/ep.h"
 #include "ep_device.h"
 #include "moe_launch.h"
@@ -124,7 +127,7 @@ __device__ __forceinline__ double exp64(double x) {
     p = __builtin_fma(p, r, 1.0);
     return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
 }
-// 1 / d for d in [1, 2^1000]: the hardware's estimate and two Newton steps.
+// 1 / d for d in [1, 2^1011]: the hardware's estimate and two Newton steps.
 __device__ __forceinline__ double reciprocal64(double d) {
     double r = __builtin_amdgcn_rcp(d);
     r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
@@ -335,7 +338,10 @@ __global__ __launch_bounds__(kWaves* kWave, kByChoice&& C == 16 ? 3 : 1) void ro
                     for (int c = 0; c < C; ++c) choice[c] = -kInf;
                 }
             } else {
-                // Any size: through shared memory, a lane to a group.
+                // Any size: through shared memory, a lane to a group, and every lane
+                // compares all groups with all (bf16, 160 experts in 8 groups, top 6, by
+                // logits: 7.6 us for one token, 11.7 for 4096; fp32, 256 experts in 64
+                // groups, top 8, by scores, 4096 tokens: 207).
                 float* row = choices + (wave * kTokens + sub) * E;
 #pragma unroll
                 for (int c = 0; c < C; ++c)
@@ -566,8 +572,8 @@ hipError_t launch_lanes(const void* logits, const float* bias, int64_t T, int E,
 }
 
 // Tokens from which a row of 16 lanes takes one: it has a quarter of the
-// instructions a token, 64 lanes the shorter way through one.  Measured, 64 lanes
-// against 16 (us): 256 experts, top 8, 4.1 / 5.3 at 2048 tokens, 5.7 / 5.5 at 4096,
+// instructions a token, 64 lanes the shorter way through one.  Measured by logits,
+// and taken for scores too, 64 lanes against 16 (us): 256 experts, top 8, 4.1 / 5.3 at 2048 tokens, 5.7 / 5.5 at 4096,
 // 27.6 / 18.6 at 32768; 128 experts, top 4, 3.6 / 3.7 at 2048, 4.9 / 3.8 at 4096;
 // 64 experts, top 6, 2.9 / 3.1 at 1024, 3.3 / 3.1 at 2048.  The gradient has fewer
 // instructions to save: 256 experts 5.3 / 5.5 at 8192, 13.6 / 11.7 at 32768 (fp32,
