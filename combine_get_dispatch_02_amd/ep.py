@@ -539,10 +539,6 @@ def _need_int32(fn: str, **values: int) -> None:
             raise ValueError(f"{fn}: {name} = {v} does not fit a 32-bit argument")
 
 
-def _last(shape: torch.Size) -> int:
-    return shape[-1] if shape else 0
-
-
 def _need_logits(logits: torch.Tensor, score: str) -> None:
     if logits.dtype not in _TYPES:
         raise TypeError(f"logits must be one of {', '.join(map(str, _TYPES))}, got {logits.dtype}")
@@ -566,12 +562,13 @@ def ep_route(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
     no part in a softmax; those whose bias is are never chosen, but keep theirs.
     Where fewer than k are left the slots are empty (-1, weight 0)."""
     k, shape = int(num_topk), logits.shape
-    if (k | num_groups | topk_groups | group_top | _last(shape)) >> 31:
+    E = shape[-1] if shape else 0
+    if (k | num_groups | topk_groups | group_top | E) >> 31:
         _need_int32("ep_route", num_topk=k, num_groups=num_groups, topk_groups=topk_groups, group_top=group_top,
-                    num_experts=_last(shape))
+                    num_experts=E)
     _need_logits(logits, score)
     dev = logits.device
-    T, E = shape
+    T = shape[0]
     if bias is not None:
         _need(bias, "bias", torch.float32, dev)
         if tuple(bias.shape) != (E,):
@@ -595,24 +592,24 @@ def ep_route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights
     """Gradient of ep_route's topk_weights with respect to the logits: [T, E]
     in the logits' type, from grad_weights [T, k] fp32 and the topk_idx that
     ep_route chose.  score, renormalize and scale as in the forward call."""
-    shape = logits.shape
-    if (_last(shape) | _last(topk_idx.shape)) >> 31:
-        _need_int32("ep_route_backward", num_experts=_last(shape), num_topk=_last(topk_idx.shape))
+    shape, ids = logits.shape, topk_idx.shape
+    if shape and ids and (shape[-1] | ids[-1]) >> 31:
+        _need_int32("ep_route_backward", num_experts=shape[-1], num_topk=ids[-1])
     _need_logits(logits, score)
     dev = logits.device
     _need(topk_idx, "topk_idx", torch.int64, dev)
     _need(grad_weights, "grad_weights", torch.float32, dev)
     T, E = shape
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+    if len(ids) != 2 or ids[0] != T:
         raise ValueError("logits and topk_idx disagree on num_tokens")
-    if grad_weights.shape != topk_idx.shape:
+    if grad_weights.shape != ids:
         raise ValueError("grad_weights must have the shape of topk_idx")
     if out is None:
         out = torch.empty_like(logits)
     else:
         _check_out({"out": out}, dev, [("out", (T, E), logits.dtype, True, False)])
     _launch("ep_route_backward", dev, logits.data_ptr(), _TYPES[logits.dtype], topk_idx.data_ptr(),
-            grad_weights.data_ptr(), T, E, topk_idx.shape[1], _SCORES[score], bool(renormalize), scale,
+            grad_weights.data_ptr(), T, E, ids[1], _SCORES[score], bool(renormalize), scale,
             out.data_ptr())
     return out
 
@@ -627,18 +624,19 @@ def ep_combine_backward(grad_out: torch.Tensor, expert_out: Optional[torch.Tenso
     of the two alone, and only that one is computed.  Rows have to be distinct,
     as every dispatch makes them.  The gradient of ep_dispatch is
     ep_combine(grad_recv_x, token_row, None)."""
-    if (_last(grad_out.shape) | _last(token_row.shape)) >> 31:
-        _need_int32("ep_combine_backward", hidden=_last(grad_out.shape), num_topk=_last(token_row.shape))
+    gs, rs = grad_out.shape, token_row.shape
+    if gs and rs and (gs[-1] | rs[-1]) >> 31:
+        _need_int32("ep_combine_backward", hidden=gs[-1], num_topk=rs[-1])
     _need(grad_out, "grad_out", torch.bfloat16)
     dev = grad_out.device
     _need(token_row, "token_row", torch.int32, dev)
-    T, H = grad_out.shape
-    if token_row.dim() != 2 or token_row.shape[0] != T:
+    T, H = gs
+    if len(rs) != 2 or rs[0] != T:
         raise ValueError("grad_out and token_row disagree on num_tokens")
-    k = token_row.shape[1]
+    k = rs[1]
     if topk_weights is not None:
         _need(topk_weights, "topk_weights", torch.float32, dev)
-        if tuple(topk_weights.shape) != (T, k):
+        if topk_weights.shape != rs:
             raise ValueError("topk_weights must have the shape of token_row")
     if expert_out is not None:
         _need(expert_out, "expert_out", torch.bfloat16, dev)
@@ -676,10 +674,9 @@ def ep_expert_linear_w4(x: torch.Tensor, expert_rows: torch.Tensor, w_codes: tor
     epilogue "silu_mul": W = 2N, gate rows first, y = silu(gate) * up; "none":
     W = N.  Rows of no expert are left as they were (uninitialised unless
     `out` is given)."""
-    weights = w_codes.shape
-    if (capacity | _last(x.shape) | max(weights, default=0)) >> 31:
-        _need_int32("ep_expert_linear_w4", capacity=capacity, in_features=_last(x.shape),
-                    weights=max(weights, default=0))
+    xs, ws = x.shape, w_codes.shape
+    if len(ws) == 3 and xs and (capacity | xs[-1] | ws[0] | ws[1]) >> 31:
+        _need_int32("ep_expert_linear_w4", capacity=capacity, in_features=xs[-1], num_experts=ws[0], weight_rows=ws[1])
     _need(x, "x", torch.bfloat16)
     dev = x.device
     _need(expert_rows, "expert_rows", torch.int32, dev)
@@ -687,26 +684,26 @@ def ep_expert_linear_w4(x: torch.Tensor, expert_rows: torch.Tensor, w_codes: tor
     _need(w_scales, "w_scales", torch.uint8, dev)
     if epilogue not in _EPILOGUES:
         raise ValueError(f"epilogue must be one of {sorted(_EPILOGUES)}, got {epilogue!r}")
-    if w_codes.dim() != 3 or x.dim() not in ((2, 3) if capacity else (2,)):
+    if len(ws) != 3 or len(xs) not in ((2, 3) if capacity else (2,)):
         raise ValueError("x must be [rows, K] (or [E, capacity, K]) and w_codes [E, W, K/2]")
-    E, W = w_codes.shape[:2]
-    K = x.shape[-1]
-    if x.dim() == 3 and tuple(x.shape[:2]) != (E, capacity):
+    E, W, half = ws
+    K = xs[-1]
+    if len(xs) == 3 and xs[:2] != (E, capacity):
         raise ValueError("x must be [E, capacity, K]")
-    if w_codes.shape[2] * 2 != K or tuple(w_scales.shape) != (E, W, K // 32):
+    if half * 2 != K or w_scales.shape != (E, W, K // 32):
         raise ValueError("w_codes must be [E, W, K/2] and w_scales [E, W, K/32]")
-    if tuple(expert_rows.shape) != (E if capacity else E + 1,):
+    if expert_rows.shape != (E if capacity else E + 1,):
         raise ValueError("expert_rows must be recv_count [E]" if capacity else
                          "expert_rows must be recv_expert_offset [E+1]")
     if epilogue == "silu_mul" and W % 2:
         raise ValueError("silu_mul needs an even number of weight rows")
     N = W // 2 if epilogue == "silu_mul" else W
-    shape = (*x.shape[:-1], N)
+    shape = (*xs[:-1], N)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
         _check_out({"out": out}, dev, [("out", shape, torch.bfloat16, True, False)])
-    rows = x.shape[0] if x.dim() == 2 else x.shape[0] * x.shape[1]
+    rows = xs[0] if len(xs) == 2 else xs[0] * xs[1]
     _launch("ep_expert_linear_w4", dev, x.data_ptr(), rows, expert_rows.data_ptr(), capacity, w_codes.data_ptr(),
             w_scales.data_ptr(), E, K, N, _EPILOGUES[epilogue], out.data_ptr())
     return out
