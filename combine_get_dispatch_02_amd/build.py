@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libep.so")
 SOURCES = ["ep_api.hip", "layout.hip", "dispatch.hip", "dispatch_ht.hip", "dispatch_ll.hip",
-           "combine.hip", "route.hip", "combine_backward.hip", "expert_w4.hip"]
+           "combine.hip", "route.hip", "combine_backward.hip", "expert_w4.hip",
+           "dispatch_i8.hip", "expert_i8.hip", "moe_i8.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

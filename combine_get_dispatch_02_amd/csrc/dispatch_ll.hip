@@ -16,7 +16,7 @@
 // becomes e*cap + position, or -1 from cap on; block 0 writes the counts),
 // then the copy kernels of ep_dispatch fill the slots, skipping dropped ones.
 #include "ep_device.h"
-#include "ep_launch.h"
+#include "moe_launch.h"
 
 namespace ep {
 namespace {
@@ -61,6 +61,18 @@ hipError_t launch_dispatch_ll(const void* x, const int64_t* topk_idx, const floa
                                         rows, T, H, k, stream);
     return launch_dispatch_copy_bf16(x, token_slot, recv_q_or_x, rows, T, H, k, stream,
                                      prefetch_pays(x_bytes, true));
+}
+
+hipError_t launch_dispatch_ll_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int64_t T, int H,
+                                 int k, int E, int cap, int8_t* recv, float* recv_scales, int32_t* recv_count,
+                                 int32_t* recv_src_idx, float* recv_w, int32_t* token_slot, void* workspace,
+                                 hipStream_t stream) {
+    if (T == 0) {
+        hipLaunchKernelGGL(ll_zero_counts_kernel, dim3(1), dim3(256), 0, stream, recv_count, E);
+        return hipGetLastError();
+    }
+    return launch_dispatch_i8(x, topk_idx, topk_weights, T, H, k, E, 1, cap, recv, recv_scales, recv_src_idx, recv_w,
+                              nullptr, nullptr, recv_count, token_slot, workspace, stream);
 }
 
 }  // namespace ep

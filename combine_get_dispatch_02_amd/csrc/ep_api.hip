@@ -581,4 +581,197 @@ int ep_expert_linear_w4(const void* x, int64_t num_rows, const int32_t* expert_r
                       fn);
 }
 
+// ---- the experts' layer in 8-bit integers ---------------------------------------------
+
+// What the casts to 8-bit integers ask of their rows.
+static int check_i8(const char* fn, int hidden, const void* recv_scales) {
+    if (hidden < 16 || hidden % 16 != 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: hidden must be a positive multiple of 16", fn);
+    if (reinterpret_cast<uintptr_t>(recv_scales) & 3u)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: scales must be 4-byte aligned", fn);
+    return EP_OK;
+}
+
+int ep_dispatch_i8(const void* x, const int64_t* topk_idx, const float* topk_weights,
+                   int64_t num_tokens, int hidden, int num_topk, int num_experts, int num_ranks,
+                   int8_t* recv_x_i8, float* recv_scales, int32_t* recv_src_idx,
+                   float* recv_topk_weights, int32_t* recv_expert_offset,
+                   int32_t* recv_rank_offset, int32_t* token_row, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    const char* fn = "ep_dispatch_i8";
+    int s = check_dispatch_common(fn, x, topk_idx, num_tokens, hidden, num_topk, num_experts,
+                                  num_ranks, recv_x_i8, recv_src_idx, recv_expert_offset,
+                                  token_row, workspace, workspace_bytes);
+    if (s != EP_OK) return s;
+    s = check_i8(fn, hidden, recv_scales);
+    if (s != EP_OK) return s;
+    if (num_tokens > 0 && !recv_scales)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: recv_scales is NULL", fn);
+    return hip_status(ep::launch_dispatch_i8(x, topk_idx, topk_weights, num_tokens, hidden, num_topk,
+                                             num_experts, num_ranks, 0, recv_x_i8, recv_scales,
+                                             recv_src_idx, recv_topk_weights, recv_expert_offset,
+                                             recv_rank_offset, nullptr, token_row, workspace,
+                                             static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+int ep_dispatch_i8_cached(const void* x, const int32_t* token_row, int64_t num_tokens, int hidden,
+                          int num_topk, int8_t* recv_x_i8, float* recv_scales, int64_t recv_rows,
+                          void* stream) {
+    const char* fn = "ep_dispatch_i8_cached";
+    if (num_tokens < 0 || recv_rows < 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_tokens and recv_rows must be >= 0", fn);
+    if (num_topk < 1) return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_topk < 1", fn);
+    if (num_topk > EP_MAX_TOPK) return fail(EP_ERR_UNSUPPORTED, "%s: num_topk > %d", fn, EP_MAX_TOPK);
+    const int s = check_i8(fn, hidden, recv_scales);
+    if (s != EP_OK) return s;
+    if (num_tokens > 0 && (!x || !token_row))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (num_tokens > 0 && recv_rows > 0 && (!recv_x_i8 || !recv_scales))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: recv_x_i8 / recv_scales is NULL", fn);
+    if (num_tokens > 0 && (!aligned16(x) || (recv_rows > 0 && !aligned16(recv_x_i8))))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: x and recv_x_i8 must be 16-byte aligned", fn);
+    if (num_tokens == 0 || recv_rows == 0) return EP_OK;
+    return hip_status(ep::launch_dispatch_copy_i8(x, token_row, recv_x_i8, recv_scales, recv_rows,
+                                                  num_tokens, hidden, num_topk,
+                                                  static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+int ep_dispatch_ll_i8(const void* x, const int64_t* topk_idx, const float* topk_weights,
+                      int64_t num_tokens, int hidden, int num_topk, int num_experts, int capacity,
+                      int8_t* recv_x_i8, float* recv_scales, int32_t* recv_count,
+                      int32_t* recv_src_idx, float* recv_topk_weights, int32_t* token_slot,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ep_dispatch_ll_i8";
+    int s = check_routing(fn, topk_idx, num_tokens, num_topk, num_experts, 1);
+    if (s != EP_OK) return s;
+    if (capacity < 1) return fail(EP_ERR_INVALID_ARGUMENT, "%s: capacity < 1", fn);
+    if (static_cast<int64_t>(num_experts) * capacity > INT32_MAX)
+        return fail(EP_ERR_UNSUPPORTED, "%s: num_experts * capacity >= 2^31", fn);
+    s = check_i8(fn, hidden, recv_scales);
+    if (s != EP_OK) return s;
+    if (!recv_count) return fail(EP_ERR_INVALID_ARGUMENT, "%s: recv_count is NULL", fn);
+    if (num_tokens > 0 && (!x || !recv_x_i8 || !recv_scales || !recv_src_idx || !token_slot))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (num_tokens > 0 && (!aligned16(x) || !aligned16(recv_x_i8)))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: x and recv_x_i8 must be 16-byte aligned", fn);
+    s = check_workspace(fn, num_tokens, workspace, workspace_bytes,
+                        ep::ll_workspace_bytes(num_tokens, num_topk, num_experts));
+    if (s != EP_OK) return s;
+    return hip_status(ep::launch_dispatch_ll_i8(x, topk_idx, topk_weights, num_tokens, hidden, num_topk,
+                                                num_experts, capacity, recv_x_i8, recv_scales,
+                                                recv_count, recv_src_idx, recv_topk_weights,
+                                                token_slot, workspace, static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+// The rows of experts that ep_quantize_i8 and ep_expert_linear_i8 take.
+static int check_expert_rows(const char* fn, int64_t num_rows, int capacity, int num_experts) {
+    if (num_rows < 0 || capacity < 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_rows and capacity must be >= 0", fn);
+    if (num_rows > INT32_MAX) return fail(EP_ERR_UNSUPPORTED, "%s: num_rows >= 2^31", fn);
+    if (num_experts < 1) return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_experts < 1", fn);
+    if (num_experts > EP_MAX_EXPERTS)
+        return fail(EP_ERR_UNSUPPORTED, "%s: num_experts > %d", fn, EP_MAX_EXPERTS);
+    if (capacity > 0 && static_cast<int64_t>(num_experts) * capacity != num_rows)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: num_rows != num_experts * capacity", fn);
+    return EP_OK;
+}
+
+int ep_quantize_i8(const void* x, int64_t num_rows, int hidden, const int32_t* expert_rows,
+                   int num_experts, int capacity, int8_t* x_i8, float* x_scales, void* stream) {
+    const char* fn = "ep_quantize_i8";
+    int s = expert_rows ? check_expert_rows(fn, num_rows, capacity, num_experts)
+                        : check_expert_rows(fn, num_rows, 0, 1);
+    if (s != EP_OK) return s;
+    s = check_i8(fn, hidden, x_scales);
+    if (s != EP_OK) return s;
+    if (num_rows > 0 && (!x || !x_i8 || !x_scales))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (!aligned16(x) || !aligned16(x_i8))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: x and x_i8 must be 16-byte aligned", fn);
+    if (num_rows == 0) return EP_OK;
+    return hip_status(ep::launch_quantize_i8(x, num_rows, hidden, expert_rows, num_experts, capacity, x_i8,
+                                             x_scales, static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+// A matrix of 8-bit weights: its sizes.
+static int check_i8_matrix(const char* fn, int in_features, int out_features, const char* in, const char* out,
+                           int multiple) {
+    if (in_features < 128 || in_features % 128 != 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: %s must be a positive multiple of 128", fn, in);
+    if (in_features > EP_MAX_IN_FEATURES_I8)
+        return fail(EP_ERR_UNSUPPORTED, "%s: %s > %d", fn, in, EP_MAX_IN_FEATURES_I8);
+    if (out_features < multiple || out_features % multiple != 0)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: %s must be a positive multiple of %d", fn, out, multiple);
+    return EP_OK;
+}
+
+int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_rows,
+                        const int32_t* expert_rows, int capacity, const int8_t* w_i8,
+                        const float* w_scales, int num_experts, int in_features, int out_features,
+                        int epilogue, void* y, void* stream) {
+    const char* fn = "ep_expert_linear_i8";
+    int s = check_expert_rows(fn, num_rows, capacity, num_experts);
+    if (s != EP_OK) return s;
+    s = check_i8_matrix(fn, in_features, out_features, "in_features", "out_features", 8);
+    if (s != EP_OK) return s;
+    if (epilogue != EP_EPILOGUE_NONE && epilogue != EP_EPILOGUE_SILU_MUL)
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: unknown epilogue %d", fn, epilogue);
+    if (out_features > INT32_MAX / 2 - 256)
+        return fail(EP_ERR_UNSUPPORTED, "%s: out_features too large", fn);
+    if (num_rows > 0 && (!x_i8 || !x_scales || !expert_rows || !w_i8 || !w_scales || !y))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (!aligned16(x_i8) || !aligned16(w_i8) || !aligned16(w_scales) || !aligned16(y) ||
+        (reinterpret_cast<uintptr_t>(x_scales) & 3u))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: misaligned x_i8 / x_scales / w_i8 / w_scales / y", fn);
+    if (num_rows == 0) return EP_OK;
+    return hip_status(ep::launch_expert_linear_i8(x_i8, x_scales, num_rows, expert_rows, capacity, w_i8,
+                                                  w_scales, num_experts, in_features, out_features,
+                                                  epilogue == EP_EPILOGUE_SILU_MUL, y,
+                                                  static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+size_t ep_moe_i8_workspace_bytes(int64_t num_tokens, int num_topk, int ffn_hidden) {
+    if (num_tokens < 0 || num_topk < 1 || ffn_hidden < 1 || num_tokens > EP_MOE_MAX_SLOTS / num_topk) return 0;
+    return static_cast<size_t>(num_tokens) * num_topk * ffn_hidden * sizeof(float);
+}
+
+int ep_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int64_t num_tokens,
+              int hidden, int num_topk, int num_experts, int ffn_hidden, const int8_t* up_i8,
+              const float* up_scales, const int8_t* down_i8, const float* down_scales, void* out,
+              void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ep_moe_i8";
+    int s = check_routing(fn, topk_idx, num_tokens, num_topk, num_experts, 1);
+    if (s != EP_OK) return s;
+    static_assert(EP_MOE_MAX_SLOTS == ep::kMoeMaxSlots, "one limit");
+    if (num_tokens > EP_MOE_MAX_SLOTS / num_topk)
+        return fail(EP_ERR_UNSUPPORTED,
+                    "%s: num_tokens * num_topk > %d (dispatch, multiply and combine larger batches)", fn,
+                    EP_MOE_MAX_SLOTS);
+    s = check_i8_matrix(fn, hidden, ffn_hidden, "hidden", "ffn_hidden", 128);
+    if (s != EP_OK) return s;
+    if (ffn_hidden > EP_MAX_IN_FEATURES_I8)
+        return fail(EP_ERR_UNSUPPORTED, "%s: ffn_hidden > %d", fn, EP_MAX_IN_FEATURES_I8);
+    if (num_tokens > 0 && (!x || !up_i8 || !up_scales || !down_i8 || !down_scales || !out))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    if (!aligned16(x) || !aligned16(up_i8) || !aligned16(up_scales) || !aligned16(down_i8) ||
+        !aligned16(down_scales) || !aligned16(out))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: x, weights, their scales and out must be 16-byte aligned", fn);
+    s = check_workspace(fn, num_tokens, workspace, workspace_bytes,
+                        ep_moe_i8_workspace_bytes(num_tokens, num_topk, ffn_hidden));
+    if (s != EP_OK) return s;
+    if (num_tokens > 0 && !aligned16(workspace))
+        return fail(EP_ERR_INVALID_ARGUMENT, "%s: workspace must be 16-byte aligned", fn);
+    if (num_tokens == 0) return EP_OK;
+    return hip_status(ep::launch_moe_i8(x, topk_idx, topk_weights, static_cast<int>(num_tokens), num_topk,
+                                        num_experts, hidden, ffn_hidden, up_i8, up_scales, down_i8,
+                                        down_scales, static_cast<float*>(workspace), out,
+                                        static_cast<hipStream_t>(stream)),
+                      fn);
+}
+
 }  // extern "C"

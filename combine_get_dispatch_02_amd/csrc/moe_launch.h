@@ -33,4 +33,29 @@ hipError_t launch_expert_linear_w4(const void* x, int64_t num_rows, const int32_
                                    int capacity, const uint8_t* w_codes, const uint8_t* w_scales,
                                    int E, int K, int N, bool silu_mul, void* y, hipStream_t stream);
 
+
+// ---- the experts' layer in 8-bit integers -------------------------------------------
+// Tokens cast on their way to their receive rows (cap > 0: to padded slots), and rows
+// cast in place.
+hipError_t launch_dispatch_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int64_t T, int H,
+                              int k, int E, int R, int cap, int8_t* recv, float* recv_scales, int32_t* recv_src_idx,
+                              float* recv_w, int32_t* expert_offset, int32_t* rank_offset, int32_t* recv_count,
+                              int32_t* token_row, void* workspace, hipStream_t stream);
+hipError_t launch_dispatch_ll_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int64_t T, int H,
+                                 int k, int E, int cap, int8_t* recv, float* recv_scales, int32_t* recv_count,
+                                 int32_t* recv_src_idx, float* recv_w, int32_t* token_slot, void* workspace,
+                                 hipStream_t stream);
+hipError_t launch_dispatch_copy_i8(const void* x, const int32_t* token_row, int8_t* recv, float* recv_scales,
+                                   int64_t num_rows, int64_t T, int H, int k, hipStream_t stream);
+hipError_t launch_quantize_i8(const void* x, int64_t num_rows, int K, const int32_t* expert_rows, int E, int capacity,
+                              int8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_expert_linear_i8(const int8_t* x, const float* x_scales, int64_t num_rows,
+                                   const int32_t* expert_rows, int capacity, const int8_t* w, const float* w_scales,
+                                   int E, int K, int N, bool silu_mul, void* y, hipStream_t stream);
+constexpr int kMoeMaxSlots = 512;                  // T * k
+// The whole layer for a few tokens; h: [T*k, F] fp32 of the workspace.
+hipError_t launch_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int T, int k, int E, int H,
+                         int F, const int8_t* up, const float* up_scales, const int8_t* down, const float* down_scales,
+                         float* h, void* out, hipStream_t stream);
+
 }  // namespace ep

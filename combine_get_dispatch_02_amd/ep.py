@@ -67,10 +67,19 @@ def lib() -> ctypes.CDLL:
     L.ep_route_backward.argtypes = [P, i32, P, P, i64, i32, i32, i32, i32, f32, P, P]
     L.ep_combine_backward.argtypes = [P, P, i64, P, P, i64, i32, i32, P, P, P]
     L.ep_expert_linear_w4.argtypes = [P, i64, P, i32, P, P, i32, i32, i32, i32, P, P]
+    L.ep_dispatch_i8.argtypes = [P, P, P, i64, i32, i32, i32, i32, P, P, P, P, P, P, P, P, sz, P]
+    L.ep_dispatch_i8_cached.argtypes = [P, P, i64, i32, i32, P, P, i64, P]
+    L.ep_dispatch_ll_i8.argtypes = [P, P, P, i64, i32, i32, i32, i32, P, P, P, P, P, P, P, sz, P]
+    L.ep_quantize_i8.argtypes = [P, i64, i32, P, i32, i32, P, P, P]
+    L.ep_expert_linear_i8.argtypes = [P, P, i64, P, i32, P, P, i32, i32, i32, i32, P, P]
+    L.ep_moe_i8_workspace_bytes.argtypes = [i64, i32, i32]
+    L.ep_moe_i8_workspace_bytes.restype = sz
+    L.ep_moe_i8.argtypes = [P, P, P, i64, i32, i32, i32, i32, P, P, P, P, P, P, sz, P]
     for f in ("ep_get_dispatch_layout", "ep_dispatch", "ep_dispatch_noalloc", "ep_dispatch_fp8", "ep_combine",
               "ep_dispatch_cached", "ep_dispatch_fp8_cached", "ep_dispatch_ht", "ep_dispatch_ll",
               "ep_dispatch_ll_fp8", "ep_route", "ep_route_backward", "ep_combine_backward",
-              "ep_expert_linear_w4"):
+              "ep_expert_linear_w4", "ep_dispatch_i8", "ep_dispatch_i8_cached", "ep_dispatch_ll_i8", "ep_quantize_i8",
+              "ep_expert_linear_i8", "ep_moe_i8"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -706,6 +715,214 @@ def ep_expert_linear_w4(x: torch.Tensor, expert_rows: torch.Tensor, w_codes: tor
     rows = xs[0] if len(xs) == 2 else xs[0] * xs[1]
     _launch("ep_expert_linear_w4", dev, x.data_ptr(), rows, expert_rows.data_ptr(), capacity, w_codes.data_ptr(),
             w_scales.data_ptr(), E, K, N, _EPILOGUES[epilogue], out.data_ptr())
+    return out
+
+
+def _need_tokens(fn: str, x: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype, weights: Optional[torch.Tensor],
+                 **values: int) -> None:
+    """The tensors that the casts on the way take: x [T, H] bf16, topk_idx or
+    token_row [T, k] and topk_weights [T, k]."""
+    xs, ks = x.shape, slots.shape
+    if len(xs) != 2 or len(ks) != 2 or ks[0] != xs[0]:
+        raise ValueError(f"{fn}: x must be [T, H], topk_idx (or token_row) [T, k]")
+    _need_int32(fn, hidden=xs[1], num_topk=ks[1], **values)
+    _need(x, "x", torch.bfloat16)
+    _need(slots, "topk_idx" if dtype is torch.int64 else "token_row", dtype, x.device)
+    if weights is not None:
+        _need(weights, "topk_weights", torch.float32, x.device)
+        if weights.shape != ks:
+            raise ValueError(f"{fn}: topk_weights must have the shape of topk_idx")
+
+
+def ep_dispatch_i8(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[torch.Tensor],
+                   num_experts: int, num_ranks: int, *,
+                   out: Optional[Dict[str, torch.Tensor]] = None,
+                   workspace: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """Dispatch cast to 8-bit integers: recv_x_i8 [T*k, H] int8 (127 x / max |x|,
+    rounded) and recv_scales [T*k] fp32 (max |x| / 127), plus the same maps as
+    ep_dispatch."""
+    _need_tokens("ep_dispatch_i8", x, topk_idx, torch.int64, topk_weights, num_experts=num_experts, num_ranks=num_ranks)
+    dev, (T, H), k = x.device, x.shape, topk_idx.shape[1]
+    if out is None:
+        # A bad num_experts or num_ranks is the library's to refuse.
+        out = _dispatch_outputs(T, k, max(num_experts, 0), max(num_ranks, 0), dev, topk_weights is not None)
+        out["recv_x_i8"] = torch.empty((T * k, H), dtype=torch.int8, device=dev)
+        out["recv_scales"] = torch.empty(T * k, dtype=torch.float32, device=dev)
+    else:
+        _check_out(out, dev, _dispatch_spec(T, k, num_experts, num_ranks, H, "recv_x_i8", torch.int8, H, False)
+                   + [("recv_scales", (T * k,), torch.float32, True, True)])
+    ws = _workspace(ep_dispatch_workspace_bytes(T, k, num_experts), dev, workspace)
+    _launch("ep_dispatch_i8", dev, x.data_ptr(), topk_idx.data_ptr(), _addr(topk_weights), T, H, k, num_experts,
+            num_ranks, out["recv_x_i8"].data_ptr(), out["recv_scales"].data_ptr(), out["recv_src_idx"].data_ptr(),
+            _addr(out.get("recv_topk_weights")), out["recv_expert_offset"].data_ptr(),
+            _addr(out.get("recv_rank_offset")), out["token_row"].data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def ep_dispatch_i8_cached(x: torch.Tensor, token_row: torch.Tensor, recv_rows: int, *,
+                          out: Optional[Dict[str, torch.Tensor]] = None) -> Dict[str, torch.Tensor]:
+    """Repeat ep_dispatch_i8 with a saved map (token_row, or token_slot of a padded
+    dispatch): recv_x_i8 [recv_rows, H] and recv_scales [recv_rows]; rows that no
+    slot maps to are left as they were."""
+    _need_tokens("ep_dispatch_i8_cached", x, token_row, torch.int32, None)
+    dev, (T, H), k = x.device, x.shape, token_row.shape[1]
+    rows = int(recv_rows)
+    if out is None:
+        # A negative recv_rows is the library's to refuse.
+        out = dict(recv_x_i8=torch.empty((max(rows, 0), H), dtype=torch.int8, device=dev),
+                   recv_scales=torch.empty(max(rows, 0), dtype=torch.float32, device=dev))
+    else:
+        _check_out(out, dev, [("recv_x_i8", (rows, H), torch.int8, True, True),
+                              ("recv_scales", (rows,), torch.float32, True, True)])
+    _launch("ep_dispatch_i8_cached", dev, x.data_ptr(), token_row.data_ptr(), T, H, k, out["recv_x_i8"].data_ptr(),
+            out["recv_scales"].data_ptr(), rows)
+    return out
+
+
+def ep_dispatch_ll_i8(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[torch.Tensor],
+                      num_experts: int, capacity: int, *,
+                      out: Optional[Dict[str, torch.Tensor]] = None,
+                      workspace: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """As ep_dispatch_ll with the cast of ep_dispatch_i8: recv_x_i8 [E, capacity, H]
+    int8 and recv_scales [E, capacity]."""
+    _need_tokens("ep_dispatch_ll_i8", x, topk_idx, torch.int64, topk_weights, num_experts=num_experts, capacity=capacity)
+    dev, (T, H), k, E = x.device, x.shape, topk_idx.shape[1], num_experts
+    spec = [("recv_x_i8", (E, capacity, H), torch.int8, True, False), ("recv_scales", (E, capacity), torch.float32, True, False),
+            ("recv_count", (E,), torch.int32, True, False), ("recv_src_idx", (E, capacity), torch.int32, True, False),
+            ("recv_topk_weights", (E, capacity), torch.float32, False, False), ("token_slot", (T, k), torch.int32, True, False)]
+    if out is None:
+        # A bad num_experts or capacity is the library's to refuse.
+        out = {name: torch.empty([max(d, 0) for d in shape], dtype=dtype, device=dev)
+               for name, shape, dtype, required, _ in spec if required or topk_weights is not None}
+    else:
+        _check_out(out, dev, spec)
+    ws = _workspace(ep_dispatch_ll_workspace_bytes(T, k, E), dev, workspace)
+    _launch("ep_dispatch_ll_i8", dev, x.data_ptr(), topk_idx.data_ptr(), _addr(topk_weights), T, H, k, E, capacity,
+            out["recv_x_i8"].data_ptr(), out["recv_scales"].data_ptr(), out["recv_count"].data_ptr(),
+            out["recv_src_idx"].data_ptr(), _addr(out.get("recv_topk_weights")), out["token_slot"].data_ptr(),
+            ws.data_ptr(), ws.numel())
+    return out
+
+
+def ep_quantize_i8(x: torch.Tensor, expert_rows: Optional[torch.Tensor] = None, *, capacity: int = 0,
+                   out: Optional[Dict[str, torch.Tensor]] = None) -> Dict[str, torch.Tensor]:
+    """The cast of ep_dispatch_i8 for rows where they are: x_i8 (int8, the shape of x)
+    and x_scales [rows] fp32 of x [rows, K] (or [E, capacity, K]) bf16.  expert_rows
+    None: all rows; else the rows of experts, as ep_expert_linear_i8 takes them
+    (recv_expert_offset [E+1], or with a capacity recv_count [E]), and the others are
+    left as they were (uninitialised unless `out` is given)."""
+    shape = x.shape
+    if len(shape) not in ((2, 3) if capacity else (2,)):
+        raise ValueError("x must be [rows, K] (or [E, capacity, K])")
+    _need_int32("ep_quantize_i8", capacity=capacity, hidden=shape[-1])
+    _need(x, "x", torch.bfloat16)
+    dev = x.device
+    E = 0
+    if expert_rows is not None:
+        _need(expert_rows, "expert_rows", torch.int32, dev)
+        if expert_rows.dim() != 1 or (not capacity and not len(expert_rows)):
+            raise ValueError("expert_rows must be recv_count [E]" if capacity else
+                             "expert_rows must be recv_expert_offset [E+1]")
+        E = len(expert_rows) if capacity else len(expert_rows) - 1
+        if len(shape) == 3 and shape[:2] != (E, capacity):
+            raise ValueError("x must be [E, capacity, K]")
+    elif capacity:
+        raise ValueError("a capacity needs expert_rows")
+    if out is None:
+        out = dict(x_i8=torch.empty(shape, dtype=torch.int8, device=dev),
+                   x_scales=torch.empty(shape[:-1], dtype=torch.float32, device=dev))
+    else:
+        _check_out(out, dev, [("x_i8", tuple(shape), torch.int8, True, False),
+                              ("x_scales", tuple(shape[:-1]), torch.float32, True, False)])
+    rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
+    _launch("ep_quantize_i8", dev, x.data_ptr(), rows, shape[-1], _addr(expert_rows), E, capacity,
+            out["x_i8"].data_ptr(), out["x_scales"].data_ptr())
+    return out
+
+
+def ep_expert_linear_i8(x_i8: torch.Tensor, x_scales: torch.Tensor, expert_rows: torch.Tensor, w_i8: torch.Tensor,
+                        w_scales: torch.Tensor, *, capacity: int = 0, epilogue: str = "none",
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The experts' products over dispatched rows in 8-bit integers: y [rows, N] bf16
+    from x_i8 [rows, K] with x_scales [rows], and w_i8 [E, W, K] with w_scales
+    [E, W].  capacity 0: x_i8 and x_scales are ep_dispatch_i8's and expert_rows its
+    recv_expert_offset [E+1]; else they are ep_dispatch_ll_i8's, as [E, capacity, K]
+    and [E, capacity] or with the first two dimensions as one, and expert_rows is
+    recv_count [E].  epilogue "silu_mul": W = 2N, gate rows first, y = silu(gate) *
+    up; "none": W = N.  Rows of no expert are left as they were (uninitialised
+    unless `out` is given)."""
+    xs, ws = x_i8.shape, w_i8.shape
+    if len(ws) != 3 or len(xs) not in ((2, 3) if capacity else (2,)):
+        raise ValueError("x_i8 must be [rows, K] (or [E, capacity, K]) and w_i8 [E, W, K]")
+    if (capacity | xs[-1] | ws[0] | ws[1]) >> 31:
+        _need_int32("ep_expert_linear_i8", capacity=capacity, in_features=xs[-1], num_experts=ws[0], weight_rows=ws[1])
+    _need(x_i8, "x_i8", torch.int8)
+    dev = x_i8.device
+    _need(x_scales, "x_scales", torch.float32, dev)
+    _need(expert_rows, "expert_rows", torch.int32, dev)
+    _need(w_i8, "w_i8", torch.int8, dev)
+    _need(w_scales, "w_scales", torch.float32, dev)
+    if epilogue not in _EPILOGUES:
+        raise ValueError(f"epilogue must be one of {sorted(_EPILOGUES)}, got {epilogue!r}")
+    E, W, K = ws
+    if xs[-1] != K or w_scales.shape != (E, W):
+        raise ValueError("x_i8 must have rows of w_i8's K, and w_scales be [E, W]")
+    if len(xs) == 3 and xs[:2] != (E, capacity):
+        raise ValueError("x_i8 must be [E, capacity, K]")
+    if x_scales.shape != xs[:-1]:
+        raise ValueError("x_scales must be one scale for each row of x_i8")
+    if expert_rows.shape != (E if capacity else E + 1,):
+        raise ValueError("expert_rows must be recv_count [E]" if capacity else
+                         "expert_rows must be recv_expert_offset [E+1]")
+    if epilogue == "silu_mul" and W % 2:
+        raise ValueError("silu_mul needs an even number of weight rows")
+    N = W // 2 if epilogue == "silu_mul" else W
+    shape = (*xs[:-1], N)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out({"out": out}, dev, [("out", shape, torch.bfloat16, True, False)])
+    rows = xs[0] if len(xs) == 2 else xs[0] * xs[1]
+    _launch("ep_expert_linear_i8", dev, x_i8.data_ptr(), x_scales.data_ptr(), rows, expert_rows.data_ptr(), capacity,
+            w_i8.data_ptr(), w_scales.data_ptr(), E, K, N, _EPILOGUES[epilogue], out.data_ptr())
+    return out
+
+
+def ep_moe_i8_workspace_bytes(num_tokens: int, num_topk: int, ffn_hidden: int) -> int:
+    return int(lib().ep_moe_i8_workspace_bytes(num_tokens, num_topk, ffn_hidden))
+
+
+def ep_moe_i8(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[torch.Tensor], up_i8: torch.Tensor,
+              up_scales: torch.Tensor, down_i8: torch.Tensor, down_scales: torch.Tensor, *,
+              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The whole layer for a few tokens (T*k <= 512 slots) in two launches: out [T, H]
+    bf16 of x [T, H] bf16, topk_idx [T, k] int64 (-1: empty slot) and topk_weights
+    [T, k] (None: all 1), with the experts' weights in 8-bit integers: up_i8
+    [E, 2F, H] (gate rows first) with up_scales [E, 2F], down_i8 [E, H, F] with
+    down_scales [E, H].  Larger batches go through ep_dispatch_i8,
+    ep_expert_linear_i8, ep_quantize_i8, ep_expert_linear_i8 and ep_combine."""
+    us, ds = up_i8.shape, down_i8.shape
+    if x.dim() != 2 or len(us) != 3 or len(ds) != 3:
+        raise ValueError("x must be [T, H], up_i8 [E, 2F, H] and down_i8 [E, H, F]")
+    (T, H), (E, _, F) = x.shape, ds
+    if (E | H | F) >> 31:
+        _need_int32("ep_moe_i8", num_experts=E, hidden=H, ffn_hidden=F)
+    _need_tokens("ep_moe_i8", x, topk_idx, torch.int64, topk_weights)
+    dev, k = x.device, topk_idx.shape[1]
+    _need(up_i8, "up_i8", torch.int8, dev)
+    _need(up_scales, "up_scales", torch.float32, dev)
+    _need(down_i8, "down_i8", torch.int8, dev)
+    _need(down_scales, "down_scales", torch.float32, dev)
+    if us != (E, 2 * F, H) or ds[1] != H or up_scales.shape != us[:2] or down_scales.shape != ds[:2]:
+        raise ValueError("up_i8 must be [E, 2F, H], up_scales [E, 2F], down_i8 [E, H, F] and down_scales [E, H]")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out({"out": out}, dev, [("out", (T, H), torch.bfloat16, True, False)])
+    # (0 bytes of a batch that the library refuses.)
+    ws = _workspace(ep_moe_i8_workspace_bytes(T, k, F), dev, workspace)
+    _launch("ep_moe_i8", dev, x.data_ptr(), topk_idx.data_ptr(), _addr(topk_weights), T, H, k, E, F, up_i8.data_ptr(),
+            up_scales.data_ptr(), down_i8.data_ptr(), down_scales.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 

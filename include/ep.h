@@ -466,6 +466,116 @@ int ep_expert_linear_w4(const void* x, int64_t num_rows, const int32_t* expert_r
                         const uint8_t* w_codes, const uint8_t* w_scales, int num_experts,
                         int in_features, int out_features, int epilogue, void* y, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The experts' layer in 8-bit integers: a scale per token, a scale per weight row.
+ *
+ * The cast of a row x (bf16), a = max |x|:
+ *   scale = a / 127 (fp32),  code = 127 * x / a, of the exact quotient, rounded to
+ *   the nearest integer, halves to even (|code| <= 127; 0 where a == 0).
+ * A row that holds an infinity or a NaN has scale a / 127 (inf or NaN) and codes 0:
+ * every product with it is NaN.
+ *
+ * ep_dispatch_i8 -- ep_dispatch with this cast.  Every row of a token receives the
+ * same codes and scale:
+ *   recv_x_i8    [T*k, H] int8 out (16-byte aligned)
+ *   recv_scales  [T*k]    fp32 out
+ * All other arguments and the workspace as ep_dispatch.  Requires H % 16 == 0.
+ * ep_dispatch_i8_cached -- the same with a saved map, as ep_dispatch_fp8_cached
+ * (recv_scales [recv_rows]).
+ * ep_dispatch_ll_i8 -- ep_dispatch_ll with this cast: recv_x_i8 [E, capacity, H],
+ * recv_scales [E, capacity].
+ *
+ * ep_quantize_i8 -- the cast of rows where they are (between two products).
+ *   x            [num_rows, hidden] bf16  in (16-byte aligned)
+ *   expert_rows  [E+1] or [E]       int32 in, as ep_expert_linear_i8 takes it:
+ *                rows expert_rows[0] .. expert_rows[E] - 1 are cast, or (capacity > 0)
+ *                the first expert_rows[e] of each expert's region, both limited to
+ *                the rows given; no other row is read or written.  NULL: all rows
+ *                (num_experts and capacity are then ignored).
+ *   x_i8         [num_rows, hidden] int8  out (16-byte aligned)
+ *   x_scales     [num_rows]         fp32  out
+ * Requires hidden % 16 == 0, 0 <= num_rows < 2^31.  No workspace.
+ * ------------------------------------------------------------------------- */
+int ep_dispatch_i8(const void* x, const int64_t* topk_idx, const float* topk_weights,
+                   int64_t num_tokens, int hidden, int num_topk, int num_experts, int num_ranks,
+                   int8_t* recv_x_i8, float* recv_scales, int32_t* recv_src_idx,
+                   float* recv_topk_weights, int32_t* recv_expert_offset,
+                   int32_t* recv_rank_offset, int32_t* token_row, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+int ep_dispatch_i8_cached(const void* x, const int32_t* token_row, int64_t num_tokens, int hidden,
+                          int num_topk, int8_t* recv_x_i8, float* recv_scales, int64_t recv_rows,
+                          void* stream);
+
+int ep_dispatch_ll_i8(const void* x, const int64_t* topk_idx, const float* topk_weights,
+                      int64_t num_tokens, int hidden, int num_topk, int num_experts, int capacity,
+                      int8_t* recv_x_i8, float* recv_scales, int32_t* recv_count,
+                      int32_t* recv_src_idx, float* recv_topk_weights, int32_t* token_slot,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+int ep_quantize_i8(const void* x, int64_t num_rows, int hidden, const int32_t* expert_rows,
+                   int num_experts, int capacity, int8_t* x_i8, float* x_scales, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ep_expert_linear_i8 -- the experts' products over dispatched rows, both operands
+ * in 8-bit integers:
+ *   sum[r, n] = sum over i of x_i8[r, i] * w_i8[e, n, i], exactly, in 32 bits
+ *   v[r, n]   = sum * (x_scales[r] * w_scales[e, n]) in fp32
+ * for every row r of expert e, and y = bf16(v), or with EP_EPILOGUE_SILU_MUL
+ * y = bf16(silu(gate) * up) as ep_expert_linear_w4 has it.  Rows, epilogue and what
+ * is done with maps out of order as in ep_expert_linear_w4.  Codes may be any
+ * int8, -128 too.
+ *
+ *   x_i8        [num_rows, in_features]   int8  in (16-byte aligned)
+ *   x_scales    [num_rows]                fp32  in
+ *   expert_rows [E+1] or [E]              int32 in
+ *   w_i8        [E, W rows, in_features]  int8  in (16-byte aligned)
+ *   w_scales    [E, W rows]               fp32  in (16-byte aligned)
+ *   y           [num_rows, out_features]  bf16  out (16-byte aligned)
+ * Requires in_features % 128 == 0, out_features % 8 == 0, both positive,
+ * in_features <= EP_MAX_IN_FEATURES_I8, 1 <= E <= EP_MAX_EXPERTS,
+ * 0 <= num_rows < 2^31, capacity >= 0.  y must not overlap the inputs.  No workspace.
+ * ------------------------------------------------------------------------- */
+#define EP_MAX_IN_FEATURES_I8 (1 << 16)
+
+int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_rows,
+                        const int32_t* expert_rows, int capacity, const int8_t* w_i8,
+                        const float* w_scales, int num_experts, int in_features, int out_features,
+                        int epilogue, void* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ep_moe_i8 -- the whole layer for a few tokens (T*k <= EP_MOE_MAX_SLOTS slots) in
+ * two launches: what ep_dispatch_i8, ep_expert_linear_i8 (silu_mul), ep_quantize_i8,
+ * ep_expert_linear_i8 and ep_combine do in a row, reading the weights of each chosen
+ * expert once and keeping what is between them in fp32.  For each slot (t, j) with
+ * expert e = topk_idx[t, j]:
+ *   xq, xs = cast of x[t]
+ *   h  = silu(gate) * up, gate and up = sum(xq * w) * (xs * up_scales[e]) (fp32)
+ *   hq, hs = cast of h (from fp32, the quotient too)
+ *   y  = sum(hq * w) * (hs * down_scales[e])        (fp32)
+ * and out[t] = bf16(acc), acc = fmaf(topk_weights[t, j], y, acc) over j = 0 .. k-1 from
+ * +0.0f.  Empty slots add nothing; a token without any gets +0.
+ *
+ *   x             [T, H]      bf16  in (16-byte aligned)
+ *   topk_idx      [T, k]      int64 in (see "Routing slots")
+ *   topk_weights  [T, k]      fp32  in (NULL: all weights 1)
+ *   up_i8         [E, 2F, H]  int8  in, up_scales [E, 2F] fp32 in (gate rows first)
+ *   down_i8       [E, H, F]   int8  in, down_scales [E, H] fp32 in (all 16-byte aligned)
+ *   out           [T, H]      bf16  out (16-byte aligned)
+ * Requires T*k <= EP_MOE_MAX_SLOTS, H % 128 == 0, F % 128 == 0, both positive and
+ * <= EP_MAX_IN_FEATURES_I8, 1 <= E <= EP_MAX_EXPERTS, 1 <= k <= EP_MAX_TOPK.  out must
+ * not overlap the inputs.  Workspace: ep_moe_i8_workspace_bytes(T, k, F), 16-byte
+ * aligned; calls that may run at the same time need one each.
+ * ------------------------------------------------------------------------- */
+#define EP_MOE_MAX_SLOTS 512
+
+size_t ep_moe_i8_workspace_bytes(int64_t num_tokens, int num_topk, int ffn_hidden);
+
+int ep_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int64_t num_tokens,
+              int hidden, int num_topk, int num_experts, int ffn_hidden, const int8_t* up_i8,
+              const float* up_scales, const int8_t* down_i8, const float* down_scales, void* out,
+              void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
