@@ -720,8 +720,8 @@ int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_r
     if (s != EP_OK) return s;
     if (epilogue != EP_EPILOGUE_NONE && epilogue != EP_EPILOGUE_SILU_MUL)
         return fail(EP_ERR_INVALID_ARGUMENT, "%s: unknown epilogue %d", fn, epilogue);
-    if (out_features > INT32_MAX / 2 - 256)
-        return fail(EP_ERR_UNSUPPORTED, "%s: out_features too large", fn);
+    if (out_features > EP_MAX_OUT_FEATURES_I8)
+        return fail(EP_ERR_UNSUPPORTED, "%s: out_features > %d", fn, EP_MAX_OUT_FEATURES_I8);
     if (num_rows > 0 && (!x_i8 || !x_scales || !expert_rows || !w_i8 || !w_scales || !y))
         return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
     if (!aligned16(x_i8) || !aligned16(w_i8) || !aligned16(w_scales) || !aligned16(y) ||

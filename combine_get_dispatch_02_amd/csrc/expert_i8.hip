@@ -139,21 +139,30 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c, int most
     }
 }
 
-// ---- many rows per expert ----------------------------------------------------------
-// One item: up to 64 kT token rows x 256 weight rows (kSilu: 128 gate rows and their
-// 128 up rows).  Four waves, one a SIMD, two by two: each has 128 weight rows (kSilu: 64
-// of either) and 32 kT token rows, 4 kT products of 32 x 32 (v_mfma_i32_32x32x32_i8) a
-// step of 32 inputs.  Both operands come through a ring of stages of 64 inputs in shared
-// memory, loaded past the registers.
+// ---- many rows per expert: bound by the matrix unit, or by reading the weights --------
+// One item: up to 256 token rows x 256 weight rows (kSilu: 128 gate rows and their 128
+// up rows).  Four waves, one a SIMD, two by two: each has 128 weight rows (kSilu: 64 of
+// either) and half of the token rows, in tiles of 32 x 32 (v_mfma_i32_32x32x32_i8).  Both
+// operands come through two slots of 128 inputs in shared memory, loaded past the
+// registers; the loads run on from an item to the next.
 //
-// A row has 64 bytes of a stage, four places of 16; inputs 16 c .. + 15 of row r are at
-// place c ^ (r / 4 % 4), so that any 16 neighbouring rows' places c lie in different
-// banks.  A lane holds row l % 32 of either operand, and inputs 32 u + 16 (l / 32) .. +
-// 15 in step u.
+// Rows come in whole lines of 128 bytes (64 bytes of twice as many rows take a load
+// twice as long: 38 against 19 cycles a KB and CU from the L2), so a slot takes 64 KB and
+// there is room for two.  To have more on the way than one stage, a stage is worked off
+// by weight tiles: a wave keeps its token tiles of all 128 inputs in registers, and in
+// quarter q multiplies them with its weight tile q, while tile q + 1 is read and, in
+// the last quarter, the next stage's token tiles.  So a slot's parts are free again
+// one after the other, long before the stage ends, and are asked for anew 1.25 to 1.75
+// stages before they are read.
+//
+// A row has eight places of 16 bytes in a slot; inputs 16 c .. + 15 of row r are at place
+// c ^ (r / 2 % 8), so that any 16 neighbouring rows' places c lie in different banks.
+// A lane holds row l % 32 of either operand, and inputs 32 u + 16 (l / 32) .. + 15 in step
+// u of a stage's four.
 
-// 16 bytes a lane past the registers to shared memory at byte `to` + 16 lane.  By hand:
-// the compiler takes any later read of shared memory for one of what such a load
-// writes, and waits for it.  Whoever reads the bytes waits by arrive().
+// 16 (or 4) bytes a lane past the registers to shared memory at byte `to` + 16 lane
+// (+ 4 lane).  By hand: the compiler takes any later read of shared memory for one of
+// what such a load writes, and waits for it.  Whoever reads the bytes waits by arrive().
 typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void load_past(uint32_t to, const Words4& from, uint32_t lane_offset, uint32_t offset) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -163,13 +172,27 @@ __device__ __forceinline__ void load_past(uint32_t to, const Words4& from, uint3
                  : "memory");
 #endif
 }
+__device__ __forceinline__ void load_past4(uint32_t to, const Words4& from, uint32_t lane_offset) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(to), "v"(lane_offset), "s"(from)
+                 : "memory");
+#endif
+}
+// Where shared memory `p` lies in the block's.
+template <typename T>
+__device__ __forceinline__ uint32_t shared_at(T* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) T*)p));
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
+}
 __device__ __forceinline__ Words4 words(const void* p, int64_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
     const int64_t most = 0x7FFFFFFF;
-    return Words4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a))),
-                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a >> 32) & 0xFFFF)),
-                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(bytes < most ? bytes : most))),
-                  0x00020000u};
+    return Words4{uniform(static_cast<uint32_t>(a)), uniform(static_cast<uint32_t>(a >> 32) & 0xFFFFu),
+                  uniform(static_cast<uint32_t>(bytes < most ? bytes : most)), 0x00020000u};
 }
 
 // The loads behind the newest kLater have arrived in every wave, and every wave is done
@@ -181,130 +204,261 @@ __device__ __forceinline__ void arrive() {
     asm volatile("" ::: "memory");
 }
 
-constexpr int kStage = 64;                          // inputs of a stage
-constexpr int kRing = 128 * 1024;                   // bytes of shared memory for the stages
+// The same in two steps: the wave's own loads, kMore more of them on the way where `more`;
+// and the other waves, (kReads) when this one's reads are done.
+template <int kLater, int kMore>
+__device__ __forceinline__ void wait(bool more) {
+    if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLater + kMore) : "memory");
+    else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLater) : "memory");
+}
+template <bool kReads = true>
+__device__ __forceinline__ void meet() {
+    if (kReads) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
-template <bool kSilu, int kT>
-__device__ __forceinline__ void tile_item(const Call& c, int e, int64_t row0, int left, int n0, uint8_t* ring) {
-    constexpr int kTokens = 64 * kT, kBytes = (kTileWeights8 + kTokens) * kStage;
-    constexpr int kDeep = kRing / kBytes < 6 ? kRing / kBytes : 6;
-    constexpr int kLoads = 4 + kT;                  // a stage's loads of a wave
-    const int lane = lane_id(), h = lane / 32, i32 = lane % 32;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const int wy = wave / 2, wx = wave % 2;
-    const uint32_t at_ring = static_cast<uint32_t>(
-        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)ring));
+constexpr int kStage = 128;                                             // inputs of a stage
+constexpr int kTokenPart = kTileWeights8 * kStage;                      // where a slot's token rows begin
+constexpr int kSlot = (kTileWeights8 + kTileRows8) * kStage;            // bytes of a slot
+constexpr int kLoads = kLoads8;
 
-    // This wave fills weight rows 64 wave .. + 63 and token rows 16 kT wave .. on, 16 rows
-    // a load: lane l writes place l % 4 of row l / 4.  kSilu: 64 gate rows, 64 up rows, 64
-    // gate rows and 64 up rows.
-    const int64_t w0 = static_cast<int64_t>(e) * (kSilu ? 2 * c.N : c.N) + n0;
-    const bool up = kSilu && wave % 2 == 1;
-    const int base = kSilu ? wy * 64 : wave * 64, outs = c.N - n0;      // first output of this wave's weight rows
-    const int wide = outs < kTileWeights8 ? outs : kTileWeights8;
-    const Words4 wb = words(c.w + (w0 + (up ? c.N : 0)) * c.K, static_cast<int64_t>(wide) * c.K);
-    const Words4 xb = words(c.x + row0 * c.K, static_cast<int64_t>(left < kTokens ? left : kTokens) * c.K);
-    uint32_t fill[kLoads];
-    const uint32_t place = ((lane & 3) ^ (lane >> 4 & 3)) * 16;
+struct Item {
+    int e, left, n0;                                // expert, token rows, first output
+    int64_t row0;
+};
+// An expert's rows go to its tiles in equal parts, of whole 64: four tiles of 192 rows
+// end together, three of 256 and one of 10 do not.
+__device__ __forceinline__ Item item_of(const Table& t, int E, int64_t item, int columns, int outputs) {
+    const int tile = static_cast<int>(item / columns), e = expert_of(t, E, tile);
+    const int count = __builtin_amdgcn_readfirstlane(t.count[e]);
+    const int tiles = (count - 1) / kTileRows8 + 1, rows = ((count - 1) / tiles / 64 + 1) * 64;
+    const int m0 = (tile - __builtin_amdgcn_readfirstlane(t.start[e])) * rows;
+    return {e, count - m0 < rows ? count - m0 : rows,
+            static_cast<int>(item - static_cast<int64_t>(tile) * columns) * outputs,
+            __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0)};
+}
+
+// The loading side of a wave: where it reads weight rows and token rows from.  Load i
+// brings eight rows.  Of a stage's 16, 0 .. 7 bring token rows 64 wave .. + 63, and 8 + 2 q
+// and 9 + 2 q a quarter of the rows of the waves' weight tiles q: rows 32 q + 16 (wave %
+// 2) .. + 15 of half wave / 2 of the weight rows.  kSilu: of tiles 0 and 1 gate rows, of 2
+// and 3 up rows.  Rows that are not there repeat the last one.
+struct Fill {
+    Words4 w[2], x;
+    uint32_t at[kLoads];
+    int stage;
+};
+// Output (of the item's) of row r of the weight rows, 32-row tile by tile.
+template <bool kSilu>
+__device__ __forceinline__ int output_of(int r) { return kSilu ? r / 128 * 64 + r % 64 : r; }
+// The row in the slot's part that load i begins with.
+__device__ __forceinline__ int first_row(int i, int wave) {
+    return i < 8 ? wave * 64 + i * 8 : wave / 2 * 128 + (i - 8) / 2 * 32 + wave % 2 * 16 + i % 2 * 8;
+}
+template <bool kSilu>
+__device__ __forceinline__ void aim(Fill& f, const Call& c, const Item& it, int wave) {
+    int lane = lane_id();
+    asm volatile("" : "+v"(lane));
+    const int wide = c.N - it.n0 < kTileWeights8 ? c.N - it.n0 : kTileWeights8;
+    const int64_t w0 = static_cast<int64_t>(it.e) * (kSilu ? 2 * c.N : c.N) + it.n0;
+    f.w[0] = words(c.w + w0 * c.K, static_cast<int64_t>(wide) * c.K);
+    f.w[1] = kSilu ? words(c.w + (w0 + c.N) * c.K, static_cast<int64_t>(wide) * c.K) : f.w[0];
+    f.x = words(c.x + it.row0 * c.K, static_cast<int64_t>(it.left) * c.K);
+    f.stage = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int r = (i < 4 ? base + i * 16 : (wave * kT + i - 4) * 16) + lane / 4, most = i < 4 ? wide : left;
-        fill[i] = (r < most ? r : most - 1) * static_cast<uint32_t>(c.K) + place;
+        const int slot_row = first_row(i, wave) + lane / 8, r = i < 8 ? slot_row : output_of<kSilu>(slot_row);
+        const int most = i < 8 ? it.left : wide;
+        const uint32_t place = (lane % 8 ^ (slot_row / 2 % 8)) * 16;
+        f.at[i] = (r < most ? r : most - 1) * static_cast<uint32_t>(c.K) + place;
     }
-    const int stages = c.K / kStage;
-    auto ask = [&](int i, int stage, uint32_t to) {
-        const int at = (stage < stages ? stage : stages - 1) * kStage;
-        if (i < 4) load_past(to + (wave * 4 + i) * 1024, wb, fill[i], at);
-        else load_past(to + kTileWeights8 * kStage + (wave * kT + i - 4) * 1024, xb, fill[i], at);
-    };
+}
+// Load i of the stage, to the slot at byte `to`.
+template <bool kSilu>
+__device__ __forceinline__ void ask(const Fill& f, int i, uint32_t to, int wave) {
+    load_past(to + (i < 8 ? kTokenPart : 0) + first_row(i, wave) * kStage, i < 8 ? f.x : f.w[kSilu && i >= 12 ? 1 : 0],
+              f.at[i], f.stage * kStage);
+}
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t two_bf16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
+// One item of up to 64 kT token rows: its stages, of which the first lies in the slot at
+// `here`, and its results.  stored: the stores of the item before.  advance() moves the loading side on by a stage.
+template <bool kSilu, int kT, typename Advance>
+__device__ __forceinline__ void tile_item(const Call& c, const Item& it, const Fill& f, Advance advance,
+                                          const uint8_t* ring, uint32_t at_ring, const float* scales, uint32_t& here,
+                                          int& stored, int wave) {
+    // Worked out anew for each item from what the compiler may not see through, or it
+    // keeps every offset of every size of tile in registers, and those in memory.
+    int lane = lane_id();
+    asm volatile("" : "+v"(lane));
+    const int h = lane / 32, i32 = lane % 32, wy = wave / 2, wx = wave % 2;
     i32x16 acc[kT][4] = {};
-    i32x4 a[2][4], b[2][kT];
-    // Where the lane finds its inputs of step 0; those of step 1 are 32 bytes on or back.
-    const uint32_t first = (h ^ (i32 >> 2 & 1)) * 16 + (i32 >> 3 & 1) * 32 + i32 * 64;
-    // Operand g of step u: weight tile g, or token tile g - 4.
-    auto read = [&](int g, int u, uint32_t from) {
-        const uint8_t* p = ring + from + (first ^ (u * 32));
-        if (g < 4) a[u][g] = *reinterpret_cast<const i32x4*>(p + (wy * 128 + g * 32) * kStage);
-        else b[u][g - 4] = *reinterpret_cast<const i32x4*>(p + (kTileWeights8 + (wx * kT + g - 4) * 32) * kStage);
+    i32x4 a[2][4], b[4][kT];                        // [quarter % 2][step], [step][token tile]
+    // Where the lane finds its inputs of step 0; those of step u are at this ^ 32 u.
+    const uint32_t first = (h ^ (i32 >> 1 & 7)) * 16 + i32 * kStage;
+    auto read_a = [&](int q, int u, uint32_t from) {
+        a[q % 2][u] = *reinterpret_cast<const i32x4*>(ring + (first ^ (u * 32)) + from + (wy * 128 + q * 32) * kStage);
     };
-    // The products of step u, and between them reads of the other step's operands at
-    // `from` and, in step 1, the loads of stage `stage` to `to`.  (In this order: left
-    // to itself the compiler reads an operand just before its first product.)
-    auto multiply = [&](int u, uint32_t from, int stage, uint32_t to) {
+    auto read_b = [&](int u, int i, uint32_t from) {
+        b[u][i] = *reinterpret_cast<const i32x4*>(ring + (first ^ (u * 32)) + from + kTokenPart + (wx * kT + i) * 32 * kStage);
+    };
+    // Quarter q of the stage in the slot at `from` (the next one's at `next`): its
+    // products, between them reads, and its loads into this slot.  (In this
+    // order: left to itself the compiler reads an operand just before its first product.)
+    auto quarter = [&](int q, uint32_t from, uint32_t next) {
+        const int ask0 = i8_quarter(q).from, ask1 = i8_quarter(q).to;
 #pragma unroll
         for (int m = 0; m < 4 * kT; ++m) {
-            const int i = m / 4, j = m % 4;
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[u][j], b[u][i], acc[i][j], 0, 0, 0);
+            const int u = m / kT, i = m % kT;
+            acc[i][q] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q % 2][u], b[u][i], acc[i][q], 0, 0, 0);
+            if (m < 4) read_a((q + 1) % 4, m, q < 3 ? from : next);
+            if (q == 3) {                           // the tiles of step u have met their last product
+                if (i == kT - 1) {
 #pragma unroll
-            for (int g = m; g < kLoads; g += 4 * kT) {
-                read(g, 1 - u, from);
-                if (u == 1) ask(g, stage, to);
+                    for (int t = 0; t < kT; ++t) read_b(u, t, next);
+                }
             }
+            // One every second product, or where there are few in turn.
+#pragma unroll
+            for (int g = ask0; g < ask1; ++g)
+                if ((kT > 2 ? (g - ask0) * 2 : (g - ask0) % (4 * kT)) == m) ask<kSilu>(f, g, at_ring + from, wave);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    arrive<0>();                                    // the last item's loads and reads are done
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d)
+    for (int u = 0; u < 4; ++u) {
+        read_a(0, u, here);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) ask(i, d, at_ring + d * kBytes);
-    arrive<(kDeep - 1) * kLoads>();
-#pragma unroll
-    for (int g = 0; g < kLoads; ++g) read(g, 0, 0);
-    uint32_t here = 0;
+        for (int t = 0; t < kT; ++t) read_b(u, t, here);
+    }
+    // Behind quarter 3 nobody waits for its own reads of shared memory: what they read is
+    // asked for anew behind quarter 0 at the earliest.  kMore: the last item's stores, if
+    // there were as many as this one makes, and this one's two loads of scales.
+    constexpr int kStores = (kSilu ? 4 : 8) * kT, kMore = kStores + 2;
+    const int stages = c.K / kStage, early = stored == kStores ? 2 : 0;
+    static_assert(i8_quarter(0).early == 2 && i8_quarter(1).early == 2 && i8_quarter(2).early == 1 &&
+                      i8_quarter(3).early == 1, "as below");
     for (int s = 0; s < stages; ++s) {
-        const uint32_t next = here + kBytes < kDeep * kBytes ? here + kBytes : 0;
-        multiply(0, here, 0, 0);
-        // The next stage is in, and every wave has read this one.
-        arrive<(kDeep - 2) * kLoads>();
-        multiply(1, next, s + kDeep, at_ring + here);
+        const uint32_t next = here ^ kSlot;
+        quarter(0, here, next);
+        wait<i8_quarter(0).later, kMore>(s < early);
+        meet();
+        quarter(1, here, next);
+        wait<i8_quarter(1).later, kMore>(s < early);
+        meet();
+        quarter(2, here, next);
+        wait<i8_quarter(2).later, kMore>(s + 1 < early);
+        meet();
+        quarter(3, here, next);
+        wait<i8_quarter(3).later, kMore>(s + 1 < early);
+        meet<false>();
+        advance();
         here = next;
     }
+    stored = kStores;
+    // The scales are in: the loads of a stage at least came after them.
+    arrive<kLoads>();
 
     // A lane holds outputs 8 p + 4 h .. + 3 (p = 0 .. 3) of token row i32 of each 32 x 32
-    // tile.
+    // tile.  Halves of the wave exchange what they have of p and p + 1, so that each
+    // stores 16 bytes.  What is not there goes past the buffer's end, where nothing is
+    // stored, so that every wave makes the same number of stores.
+    const int outs = c.N - it.n0;
+    int n_row = c.N;
+    asm volatile("" : "+s"(n_row));
+    const Buffer y = buffer(c.y + it.row0 * c.N + it.n0, ((it.left - 1) * static_cast<int64_t>(c.N) + outs) * 2);
+    float xs[kT];
 #pragma unroll
-    for (int i = 0; i < kT; ++i) {
-        const int m = (wx * kT + i) * 32 + i32;
-        if (m >= left) break;
-        const float xs = c.x_scales[row0 + m];
-        uint16_t* out = c.y + (row0 + m) * c.N + n0;
+    for (int i = 0; i < kT; ++i) xs[i] = scales[kTileWeights8 + (wx * kT + i) * 32 + i32];
 #pragma unroll
-        for (int j = 0; j < (kSilu ? 2 : 4); ++j)
+    for (int j = 0; j < (kSilu ? 2 : 4); ++j)
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int n = wy * (kSilu ? 64 : 128) + j * 32 + 8 * p + 4 * h;
-                if (n >= outs) continue;
-                auto part = [&](int t) {
-                    return i32x4{acc[i][t][4 * p], acc[i][t][4 * p + 1], acc[i][t][4 * p + 2], acc[i][t][4 * p + 3]};
-                };
-                f32x4 v = scaled(part(j), xs, scales4(c.w_scales + w0, n));
-                if (kSilu) v = silu_mul(v, scaled(part(j + 2), xs, scales4(c.w_scales + w0 + c.N, n)));
-                store4(out + n, v);
+        for (int p = 0; p < 4; p += 2) {
+            constexpr int kSides = kSilu ? 2 : 1;   // gate and up
+            f32x4 ws[kSides][2];
+#pragma unroll
+            for (int g = 0; g < kSides; ++g)
+#pragma unroll
+                for (int d = 0; d < 2; ++d) ws[g][d] = scales4(scales, wy * 128 + (j + 2 * g) * 32 + 8 * (p + d) + 4 * h);
+            const int n = wy * (kSilu ? 64 : 128) + j * 32 + 8 * (p + h);
+#pragma unroll
+            for (int i = 0; i < kT; ++i) {
+                u32x2 two[2];
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    auto value = [&](int g) {
+                        const i32x16& v = acc[i][j + 2 * g];
+                        return scaled(i32x4{v[4 * (p + d)], v[4 * (p + d) + 1], v[4 * (p + d) + 2], v[4 * (p + d) + 3]},
+                                      xs[i], ws[g][d]);
+                    };
+                    f32x4 v = value(0);
+                    if constexpr (kSilu) v = silu_mul(v, value(1));
+                    two[d] = u32x2{two_bf16(v[0], v[1]), two_bf16(v[2], v[3])};
+                }
+                const u32x2 lo = __builtin_amdgcn_permlane32_swap(two[0][0], two[1][0], false, false);
+                const u32x2 hi = __builtin_amdgcn_permlane32_swap(two[0][1], two[1][1], false, false);
+                const int m = (wx * kT + i) * 32 + i32;
+                const uint32_t to = m < it.left && n < outs ? (m * static_cast<uint32_t>(n_row) + n) * 2 : 1u << 31;
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, y, to, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
             }
-    }
+        }
 }
 
 template <bool kSilu>
 __global__ __launch_bounds__(kThreads, 1) void tile_i8_kernel(Call c, int above) {
     constexpr int kOut = kSilu ? kTileWeights8 / 2 : kTileWeights8;
-    __shared__ __align__(1024) uint8_t ring[kRing];
+    __shared__ __align__(1024) uint8_t ring[2 * kSlot];
+    // Of an item's weight rows and token rows; the next item's come to the other.
+    __shared__ __align__(16) float scales[2][kTileWeights8 + kTileRows8];
     extern __shared__ int32_t room[];
     const Table t = make_table(room, c.expert_rows, c.E, c.capacity, c.num_rows, kTileRows8, above, INT32_MAX);
-    const int columns = (c.N + kOut - 1) / kOut;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave), lane = lane_id();
+    const int columns = (c.N + kOut - 1) / kOut, stages = c.K / kStage;
     const Share mine = share_of(static_cast<int64_t>(t.start[c.E]) * columns);
-    for (int64_t item = mine.at; item < mine.end; item += mine.step) {
-        const int tile = static_cast<int>(item / columns);
-        const int e = expert_of(t, c.E, tile);
-        const int m0 = (tile - t.start[e]) * kTileRows8, rest = t.count[e] - m0;
-        const int left = __builtin_amdgcn_readfirstlane(rest < kTileRows8 ? rest : kTileRows8);
-        const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
-        const int n0 = static_cast<int>(item - static_cast<int64_t>(tile) * columns) * kOut;
+    if (mine.at >= mine.end) return;
+    const uint32_t at_ring = shared_at(ring);
+
+    Fill f;
+    int64_t filling = mine.at;
+    aim<kSilu>(f, c, item_of(t, c.E, filling, columns, kOut), wave);
+    // Behind the last item its last stage is asked for again.
+    auto advance = [&] {
+        if (++f.stage < stages) return;
+        filling += mine.step;
+        if (filling < mine.end) aim<kSilu>(f, c, item_of(t, c.E, filling, columns, kOut), wave);
+        else f.stage = stages - 1;
+    };
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) ask<kSilu>(f, i, at_ring + d * kSlot, wave);
+        advance();
+    }
+    arrive<kLoads>();
+    uint32_t here = 0;
+    int odd = 0, stored = 0;                        // stores of the last item
+    for (int64_t item = mine.at; item < mine.end; item += mine.step, odd ^= 1) {
+        const Item it = item_of(t, c.E, item, columns, kOut);
+        const int wide = c.N - it.n0 < kTileWeights8 ? c.N - it.n0 : kTileWeights8;
+        // Scales in the order of the slot's rows.
+        const int64_t w0 = static_cast<int64_t>(it.e) * (kSilu ? 2 * c.N : c.N) + it.n0 + (kSilu && wave % 2 == 1 ? c.N : 0);
+        const int n = output_of<kSilu>(wave * 64 + lane), m = wave * 64 + lane;
+        const uint32_t to = shared_at(scales[odd]) + wave * 256;
+        load_past4(to, words(c.w_scales + w0, static_cast<int64_t>(wide) * 4), (n < wide ? n : wide - 1) * 4);
+        load_past4(to + kTileWeights8 * 4, words(c.x_scales + it.row0, static_cast<int64_t>(it.left) * 4),
+                   (m < it.left ? m : it.left - 1) * 4);
         // Products of rows that are not there would cost what the others do.
-        if (left > 128) tile_item<kSilu, 4>(c, e, row0, left, n0, ring);
-        else if (left > 64) tile_item<kSilu, 2>(c, e, row0, left, n0, ring);
-        else tile_item<kSilu, 1>(c, e, row0, left, n0, ring);
+        if (it.left > 192) tile_item<kSilu, 4>(c, it, f, advance, ring, at_ring, scales[odd], here, stored, wave);
+        else if (it.left > 128) tile_item<kSilu, 3>(c, it, f, advance, ring, at_ring, scales[odd], here, stored, wave);
+        else if (it.left > 64) tile_item<kSilu, 2>(c, it, f, advance, ring, at_ring, scales[odd], here, stored, wave);
+        else tile_item<kSilu, 1>(c, it, f, advance, ring, at_ring, scales[odd], here, stored, wave);
     }
     arrive<0>();                                    // no load may write shared memory after the block's end
 }

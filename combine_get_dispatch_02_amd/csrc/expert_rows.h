@@ -180,10 +180,10 @@ __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
 }
 
-__device__ __forceinline__ void store4(uint16_t* p, const f32x4& v) {
-    *reinterpret_cast<u32x2*>(p) =
-        u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
+__device__ __forceinline__ u32x2 four_bf16(const f32x4& v) {
+    return u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
 }
+__device__ __forceinline__ void store4(uint16_t* p, const f32x4& v) { *reinterpret_cast<u32x2*>(p) = four_bf16(v); }
 
 // Blocks for `items` at most, in whole eighths, up to `full`.
 inline unsigned blocks_for(int64_t items, int64_t full) {

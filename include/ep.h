@@ -533,10 +533,11 @@ int ep_quantize_i8(const void* x, int64_t num_rows, int hidden, const int32_t* e
  *   w_scales    [E, W rows]               fp32  in (16-byte aligned)
  *   y           [num_rows, out_features]  bf16  out (16-byte aligned)
  * Requires in_features % 128 == 0, out_features % 8 == 0, both positive,
- * in_features <= EP_MAX_IN_FEATURES_I8, 1 <= E <= EP_MAX_EXPERTS,
- * 0 <= num_rows < 2^31, capacity >= 0.  y must not overlap the inputs.  No workspace.
+ * in_features <= EP_MAX_IN_FEATURES_I8, out_features <= EP_MAX_OUT_FEATURES_I8,
+ * 1 <= E <= EP_MAX_EXPERTS, 0 <= num_rows < 2^31, capacity >= 0.  y must not overlap the inputs.  No workspace.
  * ------------------------------------------------------------------------- */
 #define EP_MAX_IN_FEATURES_I8 (1 << 16)
+#define EP_MAX_OUT_FEATURES_I8 (1 << 22)
 
 int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_rows,
                         const int32_t* expert_rows, int capacity, const int8_t* w_i8,

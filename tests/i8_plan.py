@@ -1,0 +1,39 @@
+"""csrc/i8_plan.h from Python: the header is plain C++, compiled here with g++ behind
+a C interface, so that the CPU tests and the GPU tests ask the same code as the
+library does."""
+import ctypes
+import functools
+import os
+import subprocess
+import tempfile
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "combine_get_dispatch_02_amd", "csrc")
+
+SOURCE = r"""
+#include "i8_plan.h"
+extern "C" void quarter(int q, int* out) {
+    const ep::I8Quarter s = ep::i8_quarter(q);
+    out[0] = s.from; out[1] = s.to; out[2] = s.later; out[3] = s.early;
+}
+extern "C" void plan(long long num_rows, int capacity, int E, int* out) {
+    const ep::I8Plan p = ep::i8_plan(num_rows, capacity, E);
+    out[0] = p.stream_most; out[1] = p.tile_above;
+}
+"""
+
+
+@functools.lru_cache(maxsize=None)
+def lib():
+    with tempfile.TemporaryDirectory() as d:
+        src, so = os.path.join(d, "i8_plan.cpp"), os.path.join(d, "i8_plan.so")
+        with open(src, "w") as f:
+            f.write(SOURCE)
+        subprocess.check_call(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, src, "-o", so])
+        return ctypes.CDLL(so)
+
+
+def quarter(q):
+    """(from, to, later, early)"""
+    out = (ctypes.c_int * 4)()
+    lib().quarter(q, out)
+    return tuple(out)

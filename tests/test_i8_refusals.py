@@ -82,8 +82,8 @@ LINEAR = dict(x=FAKE, xs=FAKE, rows=32, erows=FAKE, capacity=0, w=FAKE, ws=FAKE,
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), EINVAL), (dict(rows=2 ** 31), EUNSUP), (dict(capacity=-1), EINVAL), (dict(capacity=3), EINVAL), (dict(E=0), EINVAL),
     (dict(E=2049), EUNSUP), (dict(K=64), EINVAL), (dict(K=192), EINVAL), (dict(K=0), EINVAL), (dict(K=(1 << 16) + 128), EUNSUP),
-    (dict(N=0), EINVAL), (dict(N=12), EINVAL), (dict(N=2 ** 31 - 8), EUNSUP), (dict(epilogue=2), EINVAL), (dict(x=None), EINVAL),
-    (dict(xs=None), EINVAL), (dict(erows=None), EINVAL), (dict(w=None), EINVAL), (dict(ws=None), EINVAL), (dict(y=None), EINVAL),
+    (dict(N=0), EINVAL), (dict(N=12), EINVAL), (dict(N=2 ** 22 + 8), EUNSUP), (dict(N=2 ** 31 - 8), EUNSUP), (dict(epilogue=2), EINVAL),
+    (dict(x=None), EINVAL), (dict(xs=None), EINVAL), (dict(erows=None), EINVAL), (dict(w=None), EINVAL), (dict(ws=None), EINVAL), (dict(y=None), EINVAL),
     (dict(x=OFF8), EINVAL), (dict(xs=OFF2), EINVAL), (dict(w=OFF8), EINVAL), (dict(ws=OFF8), EINVAL), (dict(y=OFF8), EINVAL),
     (dict(rows=0), OK), (dict(rows=0, x=None, y=None), OK),
 ])
