@@ -21,23 +21,24 @@ __global__ __launch_bounds__(kCopyThreads) void copy_i8_kernel(const u32x4* __re
                                                                const int32_t* __restrict__ token_row, int64_t T,
                                                                int pieces, int k, int64_t num_rows,
                                                                u32x4* __restrict__ recv, float* __restrict__ scales) {
-    __shared__ uint32_t room[kCopyThreads / kWave];
+    __shared__ uint32_t room[1][kCopyThreads / kWave];
     const int lane = lane_id();
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         int mine = -1;
-        cast_row<kCopyThreads, kCopyPieces, true>(
-            x + t * pieces * 2, pieces, static_cast<int>(threadIdx.x), room,
+        const u32x4* const row[1] = {x + t * pieces * 2};
+        cast_rows<kCopyThreads, kCopyPieces, 1, true>(
+            row, pieces, static_cast<int>(threadIdx.x), room,
             [&] {
-                const int row = token_row[t * k + (lane < k ? lane : 0)];
-                mine = lane < k && row < num_rows ? row : -1;
+                const int to = token_row[t * k + (lane < k ? lane : 0)];
+                mine = lane < k && to < num_rows ? to : -1;
             },
-            [&](int p, const u32x4& codes) {
+            [&](int, int p, const u32x4& codes) {
                 for (int j = 0; j < k; ++j) {
                     const int r = read_lane(mine, j);
                     if (r >= 0) __builtin_nontemporal_store(codes, recv + static_cast<int64_t>(r) * pieces + p);
                 }
             },
-            [&](float s) {
+            [&](int, float s) {
                 if (threadIdx.x < kWave && mine >= 0) scales[mine] = s;
             });
         __syncthreads();                            // `room` is read
@@ -53,20 +54,21 @@ __global__ __launch_bounds__(kSmallThreads) void dispatch_small_i8_kernel(
     int32_t* __restrict__ token_row, int32_t* __restrict__ recv_src_idx, float* __restrict__ recv_w,
     int32_t* __restrict__ expert_offset, int32_t* __restrict__ rank_offset, int32_t* __restrict__ recv_count) {
     extern __shared__ int32_t lds[];
-    __shared__ uint32_t room[kSmallThreads / kWave];
+    __shared__ uint32_t room[1][kSmallThreads / kWave];
     int32_t* rows = lds + 2 * E + 16 + kSmallMaxK;
     const int64_t t = blockIdx.x;
-    cast_row<kSmallThreads, 1, true>(
-        x + t * pieces * 2, pieces, static_cast<int>(threadIdx.x), room,
+    const u32x4* const row[1] = {x + t * pieces * 2};
+    cast_rows<kSmallThreads, 1, 1, true>(
+        row, pieces, static_cast<int>(threadIdx.x), room,
         [&] {
             small_token_rows(topk_idx, topk_weights, T, k, E, R, cap, t, true, t == 0, token_row, recv_src_idx, recv_w,
                              expert_offset, rank_offset, recv_count, lds, rows);
         },
-        [&](int p, const u32x4& codes) {
+        [&](int, int p, const u32x4& codes) {
             for (int j = 0; j < k; ++j)
                 if (rows[j] >= 0) __builtin_nontemporal_store(codes, recv + static_cast<int64_t>(rows[j]) * pieces + p);
         },
-        [&](float s) {
+        [&](int, float s) {
             const int j = static_cast<int>(threadIdx.x);
             if (j < k && rows[j] >= 0) scales[rows[j]] = s;
         });
@@ -80,7 +82,7 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const u32x4* __restric
                                                           const int32_t* __restrict__ expert_rows, int E, int capacity,
                                                           u32x4* __restrict__ codes, float* __restrict__ scales) {
     constexpr int kRows = 256 / kRowThreads;
-    __shared__ uint32_t room[256 / kWave];
+    __shared__ uint32_t room[1][kRowThreads / kWave];
     const int thread = static_cast<int>(threadIdx.x) % kRowThreads;
     int64_t first = 0, end = num_rows;
     if (expert_rows && capacity == 0) {
@@ -96,11 +98,12 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const u32x4* __restric
             filled = static_cast<int>(r) - e * capacity < expert_rows[e];
         }
         // (Threads of one row agree, and so do those that meet at a barrier.)
+        const u32x4* const row[1] = {x + r * pieces * 2};
         if (filled)
-            cast_row<kRowThreads, kPieces, true>(
-                x + r * pieces * 2, pieces, thread, room, [] {},
-                [&](int p, const u32x4& c) { __builtin_nontemporal_store(c, codes + r * pieces + p); },
-                [&](float s) {
+            cast_rows<kRowThreads, kPieces, 1, true>(
+                row, pieces, thread, room, [] {},
+                [&](int, int p, const u32x4& c) { __builtin_nontemporal_store(c, codes + r * pieces + p); },
+                [&](int, float s) {
                     if (thread == 0) scales[r] = s;
                 });
         if (kRowThreads > kWave) __syncthreads();

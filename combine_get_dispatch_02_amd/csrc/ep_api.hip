@@ -737,7 +737,7 @@ int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_r
 
 size_t ep_moe_i8_workspace_bytes(int64_t num_tokens, int num_topk, int ffn_hidden) {
     if (num_tokens < 0 || num_topk < 1 || ffn_hidden < 1 || num_tokens > EP_MOE_MAX_SLOTS / num_topk) return 0;
-    return static_cast<size_t>(num_tokens) * num_topk * ffn_hidden * sizeof(float);
+    return ep::moe_i8_workspace_bytes(static_cast<int>(num_tokens) * num_topk, ffn_hidden);
 }
 
 int ep_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int64_t num_tokens,
@@ -754,8 +754,9 @@ int ep_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights,
                     EP_MOE_MAX_SLOTS);
     s = check_i8_matrix(fn, hidden, ffn_hidden, "hidden", "ffn_hidden", 128);
     if (s != EP_OK) return s;
-    if (ffn_hidden > EP_MAX_IN_FEATURES_I8)
-        return fail(EP_ERR_UNSUPPORTED, "%s: ffn_hidden > %d", fn, EP_MAX_IN_FEATURES_I8);
+    static_assert(EP_MOE_MAX_FFN == ep::kMoeMaxFfn, "one limit");
+    if (ffn_hidden > EP_MOE_MAX_FFN)
+        return fail(EP_ERR_UNSUPPORTED, "%s: ffn_hidden > %d", fn, EP_MOE_MAX_FFN);
     if (num_tokens > 0 && (!x || !up_i8 || !up_scales || !down_i8 || !down_scales || !out))
         return fail(EP_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
     if (!aligned16(x) || !aligned16(up_i8) || !aligned16(up_scales) || !aligned16(down_i8) ||
@@ -769,7 +770,7 @@ int ep_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights,
     if (num_tokens == 0) return EP_OK;
     return hip_status(ep::launch_moe_i8(x, topk_idx, topk_weights, static_cast<int>(num_tokens), num_topk,
                                         num_experts, hidden, ffn_hidden, up_i8, up_scales, down_i8,
-                                        down_scales, static_cast<float*>(workspace), out,
+                                        down_scales, workspace, out,
                                         static_cast<hipStream_t>(stream)),
                       fn);
 }

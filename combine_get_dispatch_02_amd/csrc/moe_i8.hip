@@ -2,7 +2,8 @@
 // in two launches.
 //
 //   up    casts the tokens, multiplies them with the gate and up rows of their
-//         experts, and leaves h = silu(gate) * up in the workspace in fp32;
+//         experts, and leaves h = silu(gate) * up in the workspace in fp32, with the
+//         largest magnitudes of every 32 of a row;
 //   down  casts h, multiplies it with the experts' down rows, and adds each token's
 //         slots with their weights.
 //
@@ -121,184 +122,269 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // place lie in different banks.
 constexpr int kPad = 16;
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 // ---- up ------------------------------------------------------------------------------
 // A block takes a run of items: 32 gate rows and their 32 up rows of an expert against
 // a tile of its slots.  Its four waves split an item's inputs and join their sums in
-// shared memory.  The tokens of a tile are cast into shared memory when its first
-// item comes.
-constexpr int kUpThreads = 256;
+// shared memory; their loads run on from one item to the next.  The tokens of a tile
+// are cast into shared memory when its first item comes.
+constexpr int kUpThreads = 256, kUpDeep = 3;
 constexpr int kUpCodes = 48 * 1024;                 // bytes of codes: two blocks a CU
+constexpr int kUpOut = 32;                          // outputs of an item
 
 int up_rows(int H) { return H + kPad > kUpCodes ? 1 : kUpCodes / (H + kPad) < 16 ? kUpCodes / (H + kPad) : 16; }
 
+// The largest |h| of a place's outputs of one item, as fp32 bits: at most[column * S +
+// place].
 __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t* __restrict__ x,
                                                                   const int64_t* __restrict__ topk_idx, int S, int k,
                                                                   int E, int H, int F, const int8_t* __restrict__ up,
                                                                   const float* __restrict__ up_scales, int rows,
-                                                                  float* __restrict__ h) {
+                                                                  float* __restrict__ h, uint32_t* __restrict__ most) {
+    constexpr int kBatch = 4;                       // rows cast at a time
     __shared__ i32x4 part[16][kWave];
     __shared__ float x_scale[16];
-    __shared__ uint32_t most[2][kUpThreads / kWave];
+    __shared__ uint32_t row_room[2][kBatch][kUpThreads / kWave], h_room[16];
     extern __shared__ __align__(16) uint8_t room[];
     uint8_t* codes = room;                          // [rows][H + kPad]
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16, stride = H + kPad;
     const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
     const Slots s = group_slots<kUpThreads>(topk_idx, S, E, rows, reinterpret_cast<int32_t*>(room + rows * stride));
-    const int columns = (F + 31) / 32;
+    const int columns = F / kUpOut;
     const int64_t items = static_cast<int64_t>(s.tiles) * columns;
     // Blocks go to the 8 chiplets in turn: neighbouring runs to the blocks of one.
     const int64_t b = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
-    int64_t item = items * b / gridDim.x;
-    const int64_t end = items * (b + 1) / gridDim.x;
-    if (item == end) return;
+    const int64_t begin = items * b / gridDim.x, end = items * (b + 1) / gridDim.x;
+    if (begin == end) return;
+    // A wave's steps of an item: inputs 128 wave + 512 i .. + 127.
+    const int steps = (H / 128 + 3) / 4;
 
-    Stream8<4, 3, false> stream;
+    // The loading side.  Past its end a wave asks for its last step again.
+    u32x4 w[kUpDeep][4][2];
     uint32_t row[4];
-    Buffer w[2];
-    const float* w_scales = nullptr;
-    int n0 = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) row[j] = (j % 2 * 16 + i16) * static_cast<uint32_t>(H) + q * 16;
+    Buffer from[2];
+    int64_t asking = begin;
+    int ask_step = 0;
+    auto aim = [&] {
+        const int tile = static_cast<int>(asking / columns), column = static_cast<int>(asking - static_cast<int64_t>(tile) * columns);
+        const int8_t* p = up + (static_cast<int64_t>(uniform(s.expert[tile])) * 2 * F + column * kUpOut) * H;
+        from[0] = buffer(p, static_cast<int64_t>(kUpOut) * H);
+        from[1] = buffer(p + static_cast<int64_t>(F) * H, static_cast<int64_t>(kUpOut) * H);
+    };
+    auto load = [&](int buf) {
+        int at = wave * 128 + ask_step * 512;
+        at = at < H ? at : H - 128;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) w[buf][j][half] = load16(from[j / 2], row[j], at + 64 * half);
+        __builtin_amdgcn_sched_barrier(0);
+        if (++ask_step == steps) {
+            if (++asking < end) {
+                ask_step = 0;
+                aim();
+            } else {
+                --asking;
+                --ask_step;
+            }
+        }
+    };
+
+    // The tile at hand: its slots' tokens, cast.  `ready` runs behind the first loads.
+    int tile = -1, count = 0, first = 0;
     const uint8_t* mine = nullptr;
-    auto weights = [&](int j) { return w[j / 2]; };
-    auto tokens = [&](int half, int at) { return *reinterpret_cast<const u32x4*>(mine + at + 64 * half); };
-    // The item's rows and first loads.
-    auto start = [&](int e, int column) {
-        n0 = column * 32;
-        const int64_t w0 = static_cast<int64_t>(e) * 2 * F + n0;
-        const int left = F - n0 < 32 ? F - n0 : 32;
-        w[0] = buffer(up + w0 * H, static_cast<int64_t>(left) * H);
-        w[1] = buffer(up + (w0 + F) * H, static_cast<int64_t>(left) * H);
-        w_scales = up_scales + w0;
+    auto cast_batch = [&](int r0, auto ready) {
+        const u32x4* from_x[kBatch];
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            const int token = uniform(s.order[first + (r0 + r < count ? r0 + r : count - 1)]) / k;
+            from_x[r] = reinterpret_cast<const u32x4*>(x + static_cast<int64_t>(token) * H);
+        }
+        cast_rows<kUpThreads, 2, kBatch>(
+            from_x, H / 16, static_cast<int>(threadIdx.x), row_room[r0 / kBatch % 2], ready,
+            [&](int r, int p, const u32x4& v) {
+                if (r0 + r < count) *reinterpret_cast<u32x4*>(codes + (r0 + r) * stride + p * 16) = v;
+            },
+            [&](int r, float scale) {
+                if (threadIdx.x == 0 && r0 + r < count) x_scale[r0 + r] = scale;
+            });
+    };
+    auto stage = [&](int now, auto ready) {
+        tile = now;
+        first = uniform(s.first[tile]);
+        count = uniform(s.first[tile + 1]) - first;
+        cast_batch(0, ready);
+        for (int r0 = kBatch; r0 < count; r0 += kBatch) cast_batch(r0, [] {});
+        mine = codes + (i16 < count ? i16 : count - 1) * stride + q * 16;
+        __syncthreads();
+    };
+
+    i32x4 acc[4] = {};
+    // The four waves' sums of an item, and its results.
+    auto finish = [&](int column) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int n = j % 2 * 16 + i16;
-            row[j] = (n < left ? n : left - 1) * static_cast<uint32_t>(H) + q * 16;
+            part[wave * 4 + j][lane] = acc[j];
+            acc[j] = i32x4{};
         }
-        stream.start(wave * 128, 512, H, row, weights, tokens);
-    };
-    int tile = -1, count = 0, first = 0;
-    for (; item < end; ++item) {
-        const int now = static_cast<int>(item / columns), column = static_cast<int>(item - static_cast<int64_t>(now) * columns);
-        if (now != tile) {
-            tile = now;
-            first = uniform(s.first[tile]);
-            count = uniform(s.first[tile + 1]) - first;
-            const int e = uniform(s.expert[tile]);
-            for (int r = 0; r < count; ++r) {
-                const int token = uniform(s.order[first + r]) / k;
-                cast_row<kUpThreads, 2, false>(
-                    reinterpret_cast<const u32x4*>(x + static_cast<int64_t>(token) * H), H / 16,
-                    static_cast<int>(threadIdx.x), most[r & 1],
-                    [&] {
-                        if (r == 0) start(e, column);
-                    },
-                    [&](int p, const u32x4& v) { *reinterpret_cast<u32x4*>(codes + r * stride + p * 16) = v; },
-                    [&](float scale) {
-                        if (threadIdx.x == 0) x_scale[r] = scale;
-                    });
-            }
-            mine = codes + (i16 < count ? i16 : count - 1) * stride + q * 16;
-            __syncthreads();
-        }
-        i32x4 acc[4] = {};
-        stream.run(wave * 128, 512, H, row, weights, tokens, acc);
-        const int n = n0 + wave * 16 + 4 * q;
-        const float* ws = w_scales + wave * 16 + 4 * q;
-        // The next item's loads go out before this one's sums are joined.
-        if (item + 1 < end && column + 1 < columns) start(uniform(s.expert[tile]), column + 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[wave * 4 + j][lane] = acc[j];
         __syncthreads();
-        if (wave < 2 && i16 < count && n < F) {
+        uint32_t m = 0u;
+        if (wave < 2 && i16 < count) {
             auto sum = [&](int j) { return part[j][lane] + part[4 + j][lane] + part[8 + j][lane] + part[12 + j][lane]; };
+            const int n = column * kUpOut + wave * 16 + 4 * q;
+            const float* ws = up_scales + static_cast<int64_t>(uniform(s.expert[tile])) * 2 * F + n;
             const i32x4 gate = sum(wave), other = sum(wave + 2);
             const f32x4 gs = *reinterpret_cast<const f32x4*>(ws), us = *reinterpret_cast<const f32x4*>(ws + F);
             const float xs = x_scale[i16];
             f32x4 v;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
                 v[c] = silu(static_cast<float>(gate[c]) * (xs * gs[c])) * (static_cast<float>(other[c]) * (xs * us[c]));
-            *reinterpret_cast<f32x4*>(h + static_cast<int64_t>(s.order[first + i16]) * F + n) = v;
+                m = larger(m, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+            }
+            *reinterpret_cast<f32x4*>(h + static_cast<int64_t>(first + i16) * F + n) = v;
         }
+        m = across_rows(m);
+        if (wave == 1 && q == 0) h_room[i16] = m;
         __syncthreads();
-    }
+        if (wave == 0 && lane < count) most[column * S + first + lane] = larger(m, h_room[lane]);
+    };
+
+    aim();
+    stage(static_cast<int>(begin / columns), [&] {
+#pragma unroll
+        for (int d = 0; d < kUpDeep; ++d) load(d);
+    });
+    int column = static_cast<int>(begin % columns), step = 0;
+    const int total = static_cast<int>(end - begin) * steps;
+    for (int g = 0; g < total; g += kUpDeep)
+#pragma unroll
+        for (int d = 0; d < kUpDeep; ++d) {
+            if (g + d < total) {
+                if (step == 0 && column == columns) {
+                    column = 0;
+                    stage(tile + 1, [] {});
+                }
+                const int at = wave * 128 + step * 512;
+                if (at < H) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const u32x4 t = *reinterpret_cast<const u32x4*>(mine + at + 64 * half);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[d][j][half]),
+                                                                           __builtin_bit_cast(i32x4, t), acc[j], 0, 0, 0);
+                    }
+                }
+                if (++step == steps) {
+                    finish(column++);
+                    step = 0;
+                }
+            }
+            load(d);
+        }
 }
 
 // ---- down ----------------------------------------------------------------------------
 // A block has kRows outputs of every token.  It takes the slots in chunks whose codes fit
-// shared memory; a chunk's products, tile after tile and 128 inputs at a time, are
-// one row of steps of which each of the eight waves takes an eighth, so that its
-// loads run on from one expert to the next.  Sums meet in shared memory by integer
-// additions.
+// half of its shared memory for them; a chunk's products, tile after tile and 128
+// inputs at a time, are one row of steps of which each of the eight waves takes an
+// eighth, so that its loads run on from one expert to the next.  Sums meet in shared
+// memory by integer additions.  The next chunk's h is asked for before a chunk's
+// products, and cast behind them.
 constexpr int kDownThreads = 512;
-constexpr int kDownCodes = 64 * 1024;
-
-// Four codes a lane and step of a row of h, cast into shared memory by one wave; its
-// scale.
-__device__ __forceinline__ float cast_h(const float* __restrict__ h, int F, uint8_t* to) {
-    constexpr int kKeep = 8;                        // vectors in registers: rows of up to 2048
-    const int lane = lane_id(), vectors = F / 4;
-    const f32x4* row = reinterpret_cast<const f32x4*>(h);
-    f32x4 v[kKeep];
-    uint32_t m = 0u;
-    for (int base = 0; base < vectors; base += kKeep * kWave) {
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int p = base + i * kWave + lane;
-            v[i] = row[p < vectors ? p : vectors - 1];
-        }
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t bits = __float_as_uint(v[i][c]) & 0x7FFFFFFFu;
-                m = m > bits ? m : bits;
-            }
-    }
-    const Cast cast = cast_of(wave_most(m));
-    for (int base = 0; base < vectors; base += kKeep * kWave) {
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int p = base + i * kWave + lane;
-            if (vectors > kKeep * kWave) v[i] = row[p < vectors ? p : vectors - 1];
-            if (p < vectors) *reinterpret_cast<uint32_t*>(to + p * 4) = four_codes(cast, v[i][0], v[i][1], v[i][2], v[i][3]);
-        }
-    }
-    return cast.scale;
-}
+constexpr int kDownCodes = 32 * 1024;               // a chunk's codes at most: 16 vectors of h a thread
+constexpr int kDownRoom = 34 * 1024;                // and the bytes they take with their padding
 
 template <int kRows>
 __global__ __launch_bounds__(kDownThreads, 2) void moe_down_i8_kernel(
-    const float* __restrict__ h, const int64_t* __restrict__ topk_idx, const float* __restrict__ topk_weights, int S,
-    int T, int k, int E, int H, int F, const int8_t* __restrict__ down, const float* __restrict__ down_scales,
-    int chunk_slots, int tile_slots, uint16_t* __restrict__ out) {
-    constexpr int kTiles = kRows / 16, kDeep = 12 / kTiles;
+    const float* __restrict__ h, const uint32_t* __restrict__ most, const int64_t* __restrict__ topk_idx,
+    const float* __restrict__ topk_weights, int S, int T, int k, int E, int H, int F, const int8_t* __restrict__ down,
+    const float* __restrict__ down_scales, int chunk_slots, int tile_slots, uint16_t* __restrict__ out) {
+    constexpr int kTiles = kRows / 16, kDeep = 8 / kTiles, kKeep = kDownCodes / 4 / kDownThreads;
     extern __shared__ __align__(16) uint8_t room[];
-    const int lane = lane_id(), q = lane / 16, i16 = lane % 16, stride = F + kPad;
-    const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
-    uint8_t* codes = room;                                                  // [chunk_slots][F + kPad]
-    int32_t* sums = reinterpret_cast<int32_t*>(room + chunk_slots * stride);    // [S][kRows]
-    float* h_scale = reinterpret_cast<float*>(sums + S * kRows);                // [S]
-    const Slots s = group_slots<kDownThreads>(topk_idx, S, E, tile_slots, reinterpret_cast<int32_t*>(h_scale + S));
-    for (int i = static_cast<int>(threadIdx.x); i < S * kRows; i += kDownThreads) sums[i] = 0;
-    const int n0 = static_cast<int>(blockIdx.x) * kRows, left = H - n0 < kRows ? H - n0 : kRows;
-    const int steps = F / 128;
+    const int lane = lane_id(), q = lane / 16, i16 = lane % 16, stride = F + kPad, me = static_cast<int>(threadIdx.x);
+    const int wave = uniform(me / kWave);
+    uint8_t* codes = room;                                                      // [2][chunk_slots][F + kPad]
+    int32_t* sums = reinterpret_cast<int32_t*>(room + 2 * chunk_slots * stride);    // [S][kRows]
+    f32x2* casts = reinterpret_cast<f32x2*>(sums + S * kRows);                  // [S] of a place: scale, 127 / a
+    const Slots s = group_slots<kDownThreads>(topk_idx, S, E, tile_slots, reinterpret_cast<int32_t*>(casts + S));
+    const int places = uniform(s.first[s.tiles]);
+    for (int i = me; i < S * kRows; i += kDownThreads) sums[i] = 0;
+    const int n0 = static_cast<int>(blockIdx.x) * kRows, steps = F / 128, vectors = F / 4;
+    const uint32_t magic = 0xFFFFFFFFu / vectors + 1;
     uint32_t row[kTiles];
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-        const int n = j * 16 + i16;
-        row[j] = (n < left ? n : left - 1) * static_cast<uint32_t>(F) + q * 16;
-    }
+    for (int j = 0; j < kTiles; ++j) row[j] = (j * 16 + i16) * static_cast<uint32_t>(F) + q * 16;
+
+    // A chunk: tiles t0 .. t1 - 1, from place p0 on.  At least one tile (tile_slots <=
+    // chunk_slots).
+    struct Chunk {
+        int t0, t1, p0, p1;
+    };
+    auto chunk_from = [&](int t0) {
+        Chunk c = {t0, t0, uniform(s.first[t0]), uniform(s.first[t0])};
+        while (c.t1 < s.tiles && uniform(s.first[c.t1 + 1]) - c.p0 <= chunk_slots) c.p1 = uniform(s.first[++c.t1]);
+        return c;
+    };
+    // A chunk's h in vectors of four, thread by thread.
+    f32x4 v[kKeep];
+    auto ask_h = [&](const Chunk& c) {
+        const int all = (c.p1 - c.p0) * vectors;
+        const f32x4* from = reinterpret_cast<const f32x4*>(h + static_cast<int64_t>(c.p0) * F);
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int at = i * kDownThreads + me;
+            v[i] = from[at < all ? at : all - 1];
+        }
+    };
+    // 127 h / a by the product with 127 / a: the quotient's own error is that of fp32.
+    auto cast_h = [&](const Chunk& c, uint8_t* to) {
+        const int all = (c.p1 - c.p0) * vectors;
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int at = i * kDownThreads + me;
+            if (at >= all) break;
+            const int p = static_cast<int>(__umulhi(at, magic));    // at / vectors: exact below 2^32 / vectors
+            const float by = casts[c.p0 + p][1];
+            uint32_t code[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) code[e] = __float_as_uint(__builtin_fmaf(v[i][e], by, 12582912.0f));
+            const uint32_t lo = __builtin_amdgcn_perm(code[1], code[0], 0x0C0C0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(code[3], code[2], 0x04000C0Cu);
+            *reinterpret_cast<uint32_t*>(to + p * stride + (at - p * vectors) * 4) = by == 0.0f ? 0u : lo | hi;
+        }
+    };
     u32x4 w[kDeep][kTiles][2];
-    for (int t0 = 0, t1; t0 < s.tiles; t0 = t1) {
-        // The tiles of this chunk: at least one, for tile_slots <= chunk_slots.
-        const int place0 = uniform(s.first[t0]);
-        for (t1 = t0 + 1; t1 < s.tiles && uniform(s.first[t1 + 1]) - place0 <= chunk_slots;) ++t1;
-        const int all = (t1 - t0) * steps, begin = all * wave / 8, end = all * (wave + 1) / 8;
-        int from = t0 + begin / steps, from_at = begin % steps, to_ask = end - begin;    // the loads' tile and step
-        Buffer wb = buffer(down, 0);
+    Chunk now = chunk_from(0);
+    if (places > 0) {
+        ask_h(now);
+        if (me < places) {
+            uint32_t m = 0u;
+#pragma unroll 8
+            for (int c = 0; c < F / kUpOut; ++c) m = larger(m, most[c * S + me]);
+            const float a = __uint_as_float(m);
+            const bool none = m < 0x04000000u || m >= 0x7F800000u;     // (127 / a stays finite from 2^-119 on)
+            casts[me] = f32x2{a / 127.0f, none ? 0.0f : 127.0f * __builtin_amdgcn_rcpf(a)};
+        }
+        __syncthreads();
+        cast_h(now, codes);
+    }
+    uint8_t* here = codes;
+    while (now.t0 < s.tiles) {
+        const int all = (now.t1 - now.t0) * steps, begin = all * wave / 8, end = all * (wave + 1) / 8;
+        const Chunk then = chunk_from(now.t1);
+        if (then.t0 < s.tiles) ask_h(then);
+        // The loads' tile and step.  Past its end a wave asks for its last step again.
+        int from = now.t0 + begin / steps, from_at = begin % steps, to_ask = end - begin;
+        Buffer wb;
         auto aim = [&] {
             const int64_t w0 = static_cast<int64_t>(uniform(s.expert[from])) * H + n0;
-            wb = buffer(down + w0 * F, static_cast<int64_t>(left) * F);
+            wb = buffer(down + w0 * F, static_cast<int64_t>(kRows) * F);
         };
         auto load = [&](int buf) {
             __builtin_amdgcn_sched_barrier(0);
@@ -307,7 +393,6 @@ __global__ __launch_bounds__(kDownThreads, 2) void moe_down_i8_kernel(
 #pragma unroll
                 for (int half = 0; half < 2; ++half) w[buf][j][half] = load16(wb, row[j], from_at * 128 + 64 * half);
             __builtin_amdgcn_sched_barrier(0);
-            // Past its end a wave asks for its last step again.
             if (--to_ask > 0 && ++from_at == steps) {
                 from_at = 0;
                 ++from;
@@ -316,37 +401,32 @@ __global__ __launch_bounds__(kDownThreads, 2) void moe_down_i8_kernel(
         };
         aim();
 #pragma unroll
-        for (int b = 0; b < kDeep; ++b) load(b);
-        for (int p = wave; p < uniform(s.first[t1]) - place0; p += kDownThreads / kWave) {
-            const int slot = uniform(s.order[place0 + p]);
-            const float scale = cast_h(h + static_cast<int64_t>(slot) * F, F, codes + p * stride);
-            if (lane == 0) h_scale[slot] = scale;
-        }
-        __syncthreads();
-        int tile = t0 + begin / steps, at = begin % steps, first = 0, count = 0;
-        const uint8_t* mine = codes;
+        for (int d = 0; d < kDeep; ++d) load(d);
+        __syncthreads();                            // the chunk's codes are there
+        int tile = now.t0 + begin / steps, at = begin % steps, first = 0, count = 0;
+        const uint8_t* mine = here;
         auto enter = [&] {
             first = uniform(s.first[tile]);
             count = uniform(s.first[tile + 1]) - first;
-            mine = codes + (first - place0 + (i16 < count ? i16 : count - 1)) * stride + q * 16;
+            mine = here + (first - now.p0 + (i16 < count ? i16 : count - 1)) * stride + q * 16;
         };
         i32x4 acc[kTiles] = {};
         if (begin < end) enter();
         for (int g = begin; g < end; g += kDeep)
 #pragma unroll
-            for (int b = 0; b < kDeep; ++b) {
-                if (g + b < end) {
+            for (int d = 0; d < kDeep; ++d) {
+                if (g + d < end) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const u32x4 t = *reinterpret_cast<const u32x4*>(mine + at * 128 + 64 * half);
 #pragma unroll
                         for (int j = 0; j < kTiles; ++j)
-                            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[b][j][half]),
+                            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[d][j][half]),
                                                                            __builtin_bit_cast(i32x4, t), acc[j], 0, 0, 0);
                     }
-                    if (++at == steps || g + b + 1 == end) {
+                    if (++at == steps || g + d + 1 == end) {
                         if (i16 < count) {
-                            int32_t* to = sums + s.order[first + i16] * kRows + 4 * q;
+                            int32_t* to = sums + (first + i16) * kRows + 4 * q;
 #pragma unroll
                             for (int j = 0; j < kTiles; ++j)
 #pragma unroll
@@ -356,58 +436,74 @@ __global__ __launch_bounds__(kDownThreads, 2) void moe_down_i8_kernel(
                         for (int j = 0; j < kTiles; ++j) acc[j] = i32x4{};
                         at = 0;
                         ++tile;
-                        if (g + b + 1 < end) enter();
+                        if (g + d + 1 < end) enter();
                     }
                 }
-                load(b);
+                load(d);
             }
-        __syncthreads();
+        // (The other half of the codes: the products of the chunk before are done.)
+        here = here == codes ? codes + chunk_slots * stride : codes;
+        if (then.t0 < s.tiles) cast_h(then, here);
+        now = then;
     }
+    // Places of the slots.
+    int32_t* place = reinterpret_cast<int32_t*>(codes);
     __syncthreads();
-    for (int i = static_cast<int>(threadIdx.x); i < T * (kRows / 2); i += kDownThreads) {
+    for (int i = me; i < S; i += kDownThreads) place[i] = -1;
+    __syncthreads();
+    for (int i = me; i < places; i += kDownThreads) place[s.order[i]] = i;
+    __syncthreads();
+    for (int i = me; i < T * (kRows / 2); i += kDownThreads) {
         const int t = i / (kRows / 2), n = i % (kRows / 2) * 2;
-        if (n >= left) continue;
         float a = 0.0f, b = 0.0f;
         for (int j = 0; j < k; ++j) {
-            const int slot = t * k + j;
-            const int64_t e = topk_idx[slot];
-            if (e < 0 || e >= E) continue;
-            const float* ws = down_scales + e * H + n0 + n;
-            const float hs = h_scale[slot], weight = topk_weights ? topk_weights[slot] : 1.0f;
-            a = __builtin_fmaf(weight, static_cast<float>(sums[slot * kRows + n]) * (hs * ws[0]), a);
-            b = __builtin_fmaf(weight, static_cast<float>(sums[slot * kRows + n + 1]) * (hs * ws[1]), b);
+            const int slot = t * k + j, p = place[slot];
+            if (p < 0) continue;
+            const float* ws = down_scales + topk_idx[slot] * H + n0 + n;
+            const float hs = casts[p][0], weight = topk_weights ? topk_weights[slot] : 1.0f;
+            a = __builtin_fmaf(weight, static_cast<float>(sums[p * kRows + n]) * (hs * ws[0]), a);
+            b = __builtin_fmaf(weight, static_cast<float>(sums[p * kRows + n + 1]) * (hs * ws[1]), b);
         }
         *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(t) * H + n0 + n) = bf16_rne(a) | bf16_rne(b) << 16;
     }
 }
 
 template <int kRows>
-hipError_t launch_down(const float* h, const int64_t* topk_idx, const float* topk_weights, int T, int k, int E, int H,
-                       int F, const int8_t* down, const float* down_scales, void* out, hipStream_t stream) {
+hipError_t launch_down(const float* h, const uint32_t* most, const int64_t* topk_idx, const float* topk_weights, int T,
+                       int k, int E, int H, int F, const int8_t* down, const float* down_scales, void* out,
+                       hipStream_t stream) {
     const int S = T * k, stride = F + kPad;
-    int chunk = stride > kDownCodes ? 1 : kDownCodes / stride;
+    static_assert(kMoeMaxFfn <= kDownCodes, "a slot's codes fit");
+    int chunk = kDownCodes / F < kDownRoom / stride ? kDownCodes / F : kDownRoom / stride;
     if (chunk > S) chunk = S;
-    const size_t lds = static_cast<size_t>(chunk) * stride + sizeof(int32_t) * S * kRows + sizeof(float) * S + slots_bytes(S, E);
-    hipLaunchKernelGGL((moe_down_i8_kernel<kRows>), dim3(static_cast<unsigned>(ceil_div(H, kRows))), dim3(kDownThreads),
-                       lds, stream, h, topk_idx, topk_weights, S, T, k, E, H, F, down, down_scales, chunk,
+    const size_t lds = 2 * static_cast<size_t>(chunk) * stride + sizeof(int32_t) * S * kRows + sizeof(f32x2) * S + slots_bytes(S, E);
+    hipLaunchKernelGGL((moe_down_i8_kernel<kRows>), dim3(static_cast<unsigned>(H / kRows)), dim3(kDownThreads), lds,
+                       stream, h, most, topk_idx, topk_weights, S, T, k, E, H, F, down, down_scales, chunk,
                        chunk < 16 ? chunk : 16, static_cast<uint16_t*>(out));
     return hipGetLastError();
 }
 
 }  // namespace
 
+size_t moe_i8_workspace_bytes(int S, int F) {
+    return sizeof(float) * S * static_cast<size_t>(F) + sizeof(uint32_t) * S * static_cast<size_t>((F + kUpOut - 1) / kUpOut);
+}
+
 hipError_t launch_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int T, int k, int E, int H,
                          int F, const int8_t* up, const float* up_scales, const int8_t* down, const float* down_scales,
-                         float* h, void* out, hipStream_t stream) {
+                         void* workspace, void* out, hipStream_t stream) {
     const int S = T * k, rows = up_rows(H);
-    const int64_t items = static_cast<int64_t>(S) * ceil_div(F, 32);
+    float* h = static_cast<float*>(workspace);
+    uint32_t* most = reinterpret_cast<uint32_t*>(h + static_cast<int64_t>(S) * F);
+    const int64_t items = static_cast<int64_t>(S) * (F / kUpOut);
     hipLaunchKernelGGL(moe_up_i8_kernel, dim3(blocks_for(items, 512)), dim3(kUpThreads),
                        static_cast<size_t>(rows) * (H + kPad) + slots_bytes(S, E), stream, static_cast<const uint16_t*>(x),
-                       topk_idx, S, k, E, H, F, up, up_scales, rows, h);
+                       topk_idx, S, k, E, H, F, up, up_scales, rows, h, most);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (H <= 4096) return launch_down<16>(h, topk_idx, topk_weights, T, k, E, H, F, down, down_scales, out, stream);
-    return launch_down<32>(h, topk_idx, topk_weights, T, k, E, H, F, down, down_scales, out, stream);
+    if (H <= 4096)
+        return launch_down<16>(h, most, topk_idx, topk_weights, T, k, E, H, F, down, down_scales, out, stream);
+    return launch_down<32>(h, most, topk_idx, topk_weights, T, k, E, H, F, down, down_scales, out, stream);
 }
 
 }  // namespace ep

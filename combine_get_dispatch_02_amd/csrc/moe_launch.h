@@ -53,9 +53,11 @@ hipError_t launch_expert_linear_i8(const int8_t* x, const float* x_scales, int64
                                    const int32_t* expert_rows, int capacity, const int8_t* w, const float* w_scales,
                                    int E, int K, int N, bool silu_mul, void* y, hipStream_t stream);
 constexpr int kMoeMaxSlots = 512;                  // T * k
-// The whole layer for a few tokens; h: [T*k, F] fp32 of the workspace.
+constexpr int kMoeMaxFfn = 1 << 15;                // F
+// The whole layer for a few tokens (S = T * k slots).
+size_t moe_i8_workspace_bytes(int S, int F);
 hipError_t launch_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int T, int k, int E, int H,
                          int F, const int8_t* up, const float* up_scales, const int8_t* down, const float* down_scales,
-                         float* h, void* out, hipStream_t stream);
+                         void* workspace, void* out, hipStream_t stream);
 
 }  // namespace ep

@@ -34,13 +34,24 @@ __device__ __forceinline__ uint32_t most_bits(uint32_t m) {
     const uint32_t lo = m << 16, hi = m & 0xFFFF0000u;
     return lo > hi ? lo : hi;
 }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// Over the wave: within rows of 16 lanes by lane moves, then across them.
+template <int kMove>
+__device__ __forceinline__ uint32_t moved(uint32_t m) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), kMove, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t across_rows(uint32_t m) {
+    const u32x2 a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = larger(a[0], a[1]);
+    const u32x2 b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return larger(b[0], b[1]);
+}
 __device__ __forceinline__ uint32_t wave_most(uint32_t m) {
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1) {
-        const uint32_t v = static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, kWave));
-        m = m > v ? m : v;
-    }
-    return m;
+    m = larger(m, moved<0xB1>(m));                  // neighbours
+    m = larger(m, moved<0x4E>(m));                  // pairs
+    m = larger(m, moved<0x141>(m));                 // halves of eight, mirrored
+    m = larger(m, moved<0x140>(m));                 // halves of sixteen, mirrored
+    return across_rows(m);
 }
 
 // A row's scale, and what its codes are computed with.
@@ -98,41 +109,48 @@ struct RowPieces {
     }
 };
 
-// The largest magnitude (fp32 bits) over the kThreads threads of a row.
-template <int kThreads>
-__device__ __forceinline__ uint32_t row_most(uint32_t m, uint32_t* room) {
-    m = wave_most(most_bits(m));
+// Codes and scales of kRows rows, handed to to(row, piece, codes) and scale(row, s).
+// `ready` runs behind the first loads.
+template <int kThreads, int kPieces, int kRows, bool kOnce = false, typename Ready, typename To, typename Scale>
+__device__ __forceinline__ void cast_rows(const u32x4* const (&rows)[kRows], int pieces, int thread,
+                                          uint32_t (&room)[kRows][kThreads / kWave], Ready ready, To to, Scale scale) {
+    constexpr int kStep = kThreads * kPieces;
+    RowPieces<kThreads, kPieces, kOnce> v[kRows];
+    uint32_t m[kRows] = {};
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) v[r].load(rows[r], pieces, 0, thread);
+    ready();
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) m[r] = v[r].most(m[r]);
+    for (int base = kStep; base < pieces; base += kStep)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            v[r].load(rows[r], pieces, base, thread);
+            m[r] = v[r].most(m[r]);
+        }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        m[r] = wave_most(most_bits(m[r]));
+        if (kThreads > kWave && lane_id() == 0) room[r][threadIdx.x / kWave] = m[r];
+    }
     if (kThreads > kWave) {
-        if (lane_id() == 0) room[threadIdx.x / kWave] = m;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kThreads / kWave; ++w) m = m > room[w] ? m : room[w];
-    }
-    return m;
-}
-
-// Codes and scale of a row, handed to to(piece, codes) and scale(s).  `ready` runs
-// behind the row's first loads.
-template <int kThreads, int kPieces, bool kOnce, typename Ready, typename To, typename Scale>
-__device__ __forceinline__ void cast_row(const u32x4* __restrict__ row, int pieces, int thread, uint32_t* room,
-                                         Ready ready, To to, Scale scale) {
-    constexpr int kStep = kThreads * kPieces;
-    RowPieces<kThreads, kPieces, kOnce> r;
-    r.load(row, pieces, 0, thread);
-    ready();
-    uint32_t m = r.most(0u);
-    for (int base = kStep; base < pieces; base += kStep) {
-        r.load(row, pieces, base, thread);
-        m = r.most(m);
-    }
-    const Cast c = cast_of(row_most<kThreads>(m, room));
-    scale(c.scale);
-    for (int base = 0; base < pieces; base += kStep) {
-        if (pieces > kStep) r.load(row, pieces, base, thread);
+        for (int r = 0; r < kRows; ++r)
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int p = base + i * kThreads + thread;
-            if (p < pieces) to(p, cast16(c, r.v[i][0], r.v[i][1]));
+            for (int w = 0; w < kThreads / kWave; ++w) m[r] = larger(m[r], room[r][w]);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const Cast c = cast_of(m[r]);
+        scale(r, c.scale);
+        for (int base = 0; base < pieces; base += kStep) {
+            if (pieces > kStep) v[r].load(rows[r], pieces, base, thread);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int p = base + i * kThreads + thread;
+                if (p < pieces) to(r, p, cast16(c, v[r].v[i][0], v[r].v[i][1]));
+            }
         }
     }
 }

@@ -552,7 +552,7 @@ int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_r
  * expert e = topk_idx[t, j]:
  *   xq, xs = cast of x[t]
  *   h  = silu(gate) * up, gate and up = sum(xq * w) * (xs * up_scales[e]) (fp32)
- *   hq, hs = cast of h (from fp32, the quotient too)
+ *   hq, hs = cast of h (from fp32, the quotient too; max |h| < 2^-119: codes 0)
  *   y  = sum(hq * w) * (hs * down_scales[e])        (fp32)
  * and out[t] = bf16(acc), acc = fmaf(topk_weights[t, j], y, acc) over j = 0 .. k-1 from
  * +0.0f.  Empty slots add nothing; a token without any gets +0.
@@ -563,12 +563,13 @@ int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_r
  *   up_i8         [E, 2F, H]  int8  in, up_scales [E, 2F] fp32 in (gate rows first)
  *   down_i8       [E, H, F]   int8  in, down_scales [E, H] fp32 in (all 16-byte aligned)
  *   out           [T, H]      bf16  out (16-byte aligned)
- * Requires T*k <= EP_MOE_MAX_SLOTS, H % 128 == 0, F % 128 == 0, both positive and
- * <= EP_MAX_IN_FEATURES_I8, 1 <= E <= EP_MAX_EXPERTS, 1 <= k <= EP_MAX_TOPK.  out must
+ * Requires T*k <= EP_MOE_MAX_SLOTS, H % 128 == 0, F % 128 == 0, both positive,
+ * H <= EP_MAX_IN_FEATURES_I8, F <= EP_MOE_MAX_FFN, 1 <= E <= EP_MAX_EXPERTS, 1 <= k <= EP_MAX_TOPK.  out must
  * not overlap the inputs.  Workspace: ep_moe_i8_workspace_bytes(T, k, F), 16-byte
  * aligned; calls that may run at the same time need one each.
  * ------------------------------------------------------------------------- */
 #define EP_MOE_MAX_SLOTS 512
+#define EP_MOE_MAX_FFN (1 << 15)
 
 size_t ep_moe_i8_workspace_bytes(int64_t num_tokens, int num_topk, int ffn_hidden);
 

@@ -115,7 +115,7 @@ def test_out_and_workspace_of_the_caller():
     layer = Layer(256, 128, 8)
     x, idx, w = layer.inputs(5, 3)
     n = ep.ep_moe_i8_workspace_bytes(5, 3, 128)
-    assert n == 5 * 3 * 128 * 4
+    assert n == 5 * 3 * (128 + 128 // 32) * 4
     ws = torch.full((n + 64,), 255, dtype=torch.uint8, device=DEV)
     room = torch.full((7, 256), 7.0, dtype=torch.bfloat16, device=DEV)
     got = layer.run(x, idx, w, out=room[1:6], workspace=ws[:n])

@@ -97,10 +97,10 @@ MOE = dict(x=FAKE, idx=FAKE, w=FAKE, T=16, H=256, k=2, E=8, F=128, up=FAKE, us=F
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), EINVAL), (dict(k=0), EINVAL), (dict(k=65), EUNSUP), (dict(T=257), EUNSUP), (dict(T=2 ** 30, k=1), EUNSUP),
     (dict(T=2 ** 62, k=4), EUNSUP), (dict(E=0), EINVAL), (dict(E=2049), EUNSUP), (dict(H=0), EINVAL), (dict(H=192), EINVAL),
-    (dict(F=0), EINVAL), (dict(F=64), EINVAL), (dict(H=65664), EUNSUP), (dict(F=65664), EUNSUP), (dict(idx=None), EINVAL),
+    (dict(F=0), EINVAL), (dict(F=64), EINVAL), (dict(H=65664), EUNSUP), (dict(F=32896), EUNSUP), (dict(idx=None), EINVAL),
     (dict(x=None), EINVAL), (dict(up=None), EINVAL), (dict(us=None), EINVAL), (dict(down=None), EINVAL), (dict(ds=None), EINVAL),
     (dict(out=None), EINVAL), (dict(x=OFF8), EINVAL), (dict(up=OFF8), EINVAL), (dict(us=OFF8), EINVAL), (dict(down=OFF8), EINVAL),
-    (dict(ds=OFF8), EINVAL), (dict(out=OFF8), EINVAL), (dict(ws=None), EWS), (dict(wsb=16 * 2 * 128 * 4 - 1), EWS), (dict(ws=OFF8), EINVAL),
+    (dict(ds=OFF8), EINVAL), (dict(out=OFF8), EINVAL), (dict(ws=None), EWS), (dict(wsb=16 * 2 * 132 * 4 - 1), EWS), (dict(ws=OFF8), EINVAL),
     (dict(T=0), OK), (dict(T=0, x=None, idx=None, ws=None, wsb=0), OK),
 ])
 def test_moe(kw, code):
@@ -108,7 +108,7 @@ def test_moe(kw, code):
 
 
 def test_moe_workspace():
-    assert ep.ep_moe_i8_workspace_bytes(64, 8, 2048) == 64 * 8 * 2048 * 4
+    assert ep.ep_moe_i8_workspace_bytes(64, 8, 2048) == 64 * 8 * (2048 + 2048 // 32) * 4
     assert ep.ep_moe_i8_workspace_bytes(65, 8, 2048) == 0 and ep.ep_moe_i8_workspace_bytes(-1, 8, 2048) == 0
 
 
