@@ -74,7 +74,7 @@ __device__ __forceinline__ f32x4 scales4(const float* scales, int n) {
 template <bool kSilu>
 __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c, int most) {
     constexpr int kOut = kSilu ? 32 : 64;           // outputs of an item
-    constexpr int kDeep = 3;
+    constexpr int kDeep = 2;
     __shared__ i32x4 part[16][kWave];
     extern __shared__ int32_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16;

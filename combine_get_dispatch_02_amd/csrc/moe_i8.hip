@@ -20,8 +20,8 @@ namespace ep {
 namespace {
 
 // ---- the slots by expert -------------------------------------------------------------
-// Tiles of up to `most` slots of one expert, in order of the experts and then of the
-// slots: every block of a launch finds the same.
+// Tiles of up to `most` slots of one expert, an expert's in order of the slots: every
+// block finds the same, and both launches the same places.
 struct Slots {
     int tiles;
     int32_t* expert;                                // [tiles]
@@ -40,9 +40,45 @@ __device__ __forceinline__ int add_bytes(uint32_t v, int a) {
     return static_cast<int>(__builtin_amdgcn_sad_u8(v, 0u, static_cast<uint32_t>(a)));
 }
 
+// At most 64 slots, one a lane: without counters, experts in the order in which the
+// slots name them first.
+__device__ __forceinline__ Slots group_few_slots(const int64_t* __restrict__ topk_idx, int S, int E, int most,
+                                                 int32_t* room) {
+    const Slots s = {0, room, room + S, room + 2 * S + 1};
+    const int lane = lane_id();
+    const int64_t e = topk_idx[lane < S ? lane : S - 1];
+    const bool valid = lane < S && e >= 0 && e < E;
+    const int id = valid ? static_cast<int>(e) : -1;
+    const uint64_t peers = match_key(id, valid, 32 - __builtin_clz(E));
+    const int count = __popcll(peers), rank = __popcll(peers & lanes_below()), tiles = (count + most - 1) / most;
+    // Tiles (high half) and slots (low half) of the experts named before; of an expert's
+    // lanes the first one counts.
+    const int mine = valid && rank == 0 ? count + (tiles << 16) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+    }
+    const int all = read_lane(upto, kWave - 1);
+    const int before = __shfl(upto - mine, valid ? __builtin_ctzll(peers) : 0);
+    if (threadIdx.x < kWave) {
+        if (valid) s.order[(before & 0xFFFF) + rank] = lane;
+        if (valid && rank == 0)
+            for (int t = 0; t < tiles; ++t) {
+                s.expert[(before >> 16) + t] = id;
+                s.first[(before >> 16) + t] = (before & 0xFFFF) + t * most;
+            }
+        if (lane == 0) s.first[all >> 16] = all & 0xFFFF;
+    }
+    __syncthreads();
+    return {__builtin_amdgcn_readfirstlane(all >> 16), s.expert, s.first, s.order};
+}
+
 template <int kThreads>
 __device__ __forceinline__ Slots group_slots(const int64_t* __restrict__ topk_idx, int S, int E, int most,
                                              int32_t* room) {
+    if (S <= kWave) return group_few_slots(topk_idx, S, E, most, room);
     constexpr int kEach = (kMoeMaxSlots + kThreads - 1) / kThreads;
     __shared__ int32_t sums[kThreads / kWave];
     const int words = count_words(S), nbits = 32 - __builtin_clz(E);
@@ -126,24 +162,28 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // ---- up ------------------------------------------------------------------------------
 // A block takes a run of items: 32 gate rows and their 32 up rows of an expert against
-// a tile of its slots.  Its four waves split an item's inputs and join their sums in
+// a tile of its slots.  Its eight waves split an item's inputs and join their sums in
 // shared memory; their loads run on from one item to the next.  The tokens of a tile
 // are cast into shared memory when its first item comes.
-constexpr int kUpThreads = 256, kUpDeep = 3;
-constexpr int kUpCodes = 48 * 1024;                 // bytes of codes: two blocks a CU
+constexpr int kUpThreads = 512, kUpWaves = kUpThreads / kWave, kUpDeep = 2;
+constexpr int kUpShared = 126 * 1024;               // bytes of a CU's 160 KB beside what is declared below
 constexpr int kUpOut = 32;                          // outputs of an item
 
-int up_rows(int H) { return H + kPad > kUpCodes ? 1 : kUpCodes / (H + kPad) < 16 ? kUpCodes / (H + kPad) : 16; }
+// Rows of a tile: as many as find room.
+int up_rows(int S, int E, int H) {
+    const int rows = (kUpShared - static_cast<int>(slots_bytes(S, E))) / (H + kPad);
+    return rows < 16 ? rows : 16;
+}
 
-// The largest |h| of a place's outputs of one item, as fp32 bits: at most[column * S +
-// place].
+// The largest |h| of a place's outputs of one item, as fp32 bits: at most[place * (F /
+// 32) + column].
 __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t* __restrict__ x,
                                                                   const int64_t* __restrict__ topk_idx, int S, int k,
                                                                   int E, int H, int F, const int8_t* __restrict__ up,
                                                                   const float* __restrict__ up_scales, int rows,
                                                                   float* __restrict__ h, uint32_t* __restrict__ most) {
     constexpr int kBatch = 4;                       // rows cast at a time
-    __shared__ i32x4 part[16][kWave];
+    __shared__ i32x4 part[kUpWaves][4][kWave];
     __shared__ float x_scale[16];
     __shared__ uint32_t row_room[2][kBatch][kUpThreads / kWave], h_room[16];
     extern __shared__ __align__(16) uint8_t room[];
@@ -157,8 +197,8 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
     const int64_t b = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
     const int64_t begin = items * b / gridDim.x, end = items * (b + 1) / gridDim.x;
     if (begin == end) return;
-    // A wave's steps of an item: inputs 128 wave + 512 i .. + 127.
-    const int steps = (H / 128 + 3) / 4;
+    // A wave's steps of an item: inputs 128 (wave + 8 i) .. + 127.
+    const int steps = (H / 128 + kUpWaves - 1) / kUpWaves;
 
     // The loading side.  Past its end a wave asks for its last step again.
     u32x4 w[kUpDeep][4][2];
@@ -175,7 +215,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
         from[1] = buffer(p + static_cast<int64_t>(F) * H, static_cast<int64_t>(kUpOut) * H);
     };
     auto load = [&](int buf) {
-        int at = wave * 128 + ask_step * 512;
+        int at = (wave + ask_step * kUpWaves) * 128;
         at = at < H ? at : H - 128;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -204,7 +244,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
             const int token = uniform(s.order[first + (r0 + r < count ? r0 + r : count - 1)]) / k;
             from_x[r] = reinterpret_cast<const u32x4*>(x + static_cast<int64_t>(token) * H);
         }
-        cast_rows<kUpThreads, 2, kBatch>(
+        cast_rows<kUpThreads, 1, kBatch>(
             from_x, H / 16, static_cast<int>(threadIdx.x), row_room[r0 / kBatch % 2], ready,
             [&](int r, int p, const u32x4& v) {
                 if (r0 + r < count) *reinterpret_cast<u32x4*>(codes + (r0 + r) * stride + p * 16) = v;
@@ -224,21 +264,32 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
     };
 
     i32x4 acc[4] = {};
-    // The four waves' sums of an item, and its results.
+    // The scales of an item's rows, asked for while the item before is finished.
+    f32x4 gs, us;
+    auto ask_scales = [&](int64_t item) {
+        const int t = static_cast<int>(item / columns), column = static_cast<int>(item - static_cast<int64_t>(t) * columns);
+        const float* ws = up_scales + static_cast<int64_t>(uniform(s.expert[t])) * 2 * F + column * kUpOut + wave % 2 * 16 + 4 * q;
+        gs = *reinterpret_cast<const f32x4*>(ws);
+        us = *reinterpret_cast<const f32x4*>(ws + F);
+    };
+    // The waves' sums of an item, and its results.
     auto finish = [&](int column) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            part[wave * 4 + j][lane] = acc[j];
+            part[wave][j][lane] = acc[j];
             acc[j] = i32x4{};
         }
         __syncthreads();
         uint32_t m = 0u;
         if (wave < 2 && i16 < count) {
-            auto sum = [&](int j) { return part[j][lane] + part[4 + j][lane] + part[8 + j][lane] + part[12 + j][lane]; };
+            auto sum = [&](int j) {
+                i32x4 v = part[0][j][lane];
+#pragma unroll
+                for (int o = 1; o < kUpWaves; ++o) v += part[o][j][lane];
+                return v;
+            };
             const int n = column * kUpOut + wave * 16 + 4 * q;
-            const float* ws = up_scales + static_cast<int64_t>(uniform(s.expert[tile])) * 2 * F + n;
             const i32x4 gate = sum(wave), other = sum(wave + 2);
-            const f32x4 gs = *reinterpret_cast<const f32x4*>(ws), us = *reinterpret_cast<const f32x4*>(ws + F);
             const float xs = x_scale[i16];
             f32x4 v;
 #pragma unroll
@@ -251,14 +302,16 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
         m = across_rows(m);
         if (wave == 1 && q == 0) h_room[i16] = m;
         __syncthreads();
-        if (wave == 0 && lane < count) most[column * S + first + lane] = larger(m, h_room[lane]);
+        if (wave == 0 && lane < count) most[(first + lane) * static_cast<int64_t>(columns) + column] = larger(m, h_room[lane]);
     };
 
     aim();
     stage(static_cast<int>(begin / columns), [&] {
+        ask_scales(begin);
 #pragma unroll
         for (int d = 0; d < kUpDeep; ++d) load(d);
     });
+    int64_t item = begin;
     int column = static_cast<int>(begin % columns), step = 0;
     const int total = static_cast<int>(end - begin) * steps;
     for (int g = 0; g < total; g += kUpDeep)
@@ -269,7 +322,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
                     column = 0;
                     stage(tile + 1, [] {});
                 }
-                const int at = wave * 128 + step * 512;
+                const int at = (wave + step * kUpWaves) * 128;
                 if (at < H) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -283,6 +336,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
                 if (++step == steps) {
                     finish(column++);
                     step = 0;
+                    ask_scales(item + 1 < end ? ++item : item);
                 }
             }
             load(d);
@@ -291,140 +345,228 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
 
 // ---- down ----------------------------------------------------------------------------
 // A block has kRows outputs of every token.  It takes the slots in chunks whose codes fit
-// half of its shared memory for them; a chunk's products, tile after tile and 128
-// inputs at a time, are one row of steps of which each of the eight waves takes an
-// eighth, so that its loads run on from one expert to the next.  Sums meet in shared
-// memory by integer additions.  The next chunk's h is asked for before a chunk's
-// products, and cast behind them.
-constexpr int kDownThreads = 512;
-constexpr int kDownCodes = 32 * 1024;               // a chunk's codes at most: 16 vectors of h a thread
+// half of its shared memory for them.  Eight waves multiply: a chunk's products, tile
+// after tile and 128 inputs at a time, are one row of steps of which each takes an
+// eighth; their loads run on from one chunk to the next, and sums meet in shared memory
+// by integer additions.  Eight more waves cast the next chunk's h meanwhile.  (The same
+// by all waves between the chunks had loads on the way for a third of the time only:
+// 64 tokens over 64 experts, 1024 -> 4096, 126 us.)
+constexpr int kDownWaves = 8, kCastWaves = 8, kDownThreads = (kDownWaves + kCastWaves) * kWave;
+constexpr int kDownCodes = 32 * 1024;               // a chunk's codes at most
 constexpr int kDownRoom = 34 * 1024;                // and the bytes they take with their padding
 
+// Tiles t0 .. t1 - 1, with places p0 .. p1 - 1.
+struct Chunk {
+    int t0, t1, p0, p1;
+};
+// The chunk that begins with tile t0: as many tiles as have at most `slots` places, and
+// that is at least one.  Every lane asks about one tile in `step`, then about one of
+// those between.
+__device__ __forceinline__ Chunk chunk_from(const Slots& s, int t0, int slots) {
+    Chunk c = {t0, t0, 0, 0};
+    if (t0 >= s.tiles) return c;
+    const int step = (kMoeMaxSlots + kWave - 1) / kWave, lane = lane_id();
+    c.p0 = uniform(s.first[t0]);
+    auto fits = [&](int t) { return t <= s.tiles && s.first[t <= s.tiles ? t : s.tiles] - c.p0 <= slots; };
+    const int t = t0 + (__popcll(ballot(fits(t0 + lane * step))) - 1) * step;
+    c.t1 = uniform(t + __popcll(ballot(lane < step && fits(t + lane))) - 1);
+    c.p1 = uniform(s.first[c.t1]);
+    return c;
+}
+
 template <int kRows>
-__global__ __launch_bounds__(kDownThreads, 2) void moe_down_i8_kernel(
+__global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_kernel(
     const float* __restrict__ h, const uint32_t* __restrict__ most, const int64_t* __restrict__ topk_idx,
     const float* __restrict__ topk_weights, int S, int T, int k, int E, int H, int F, const int8_t* __restrict__ down,
     const float* __restrict__ down_scales, int chunk_slots, int tile_slots, uint16_t* __restrict__ out) {
-    constexpr int kTiles = kRows / 16, kDeep = 8 / kTiles, kKeep = kDownCodes / 4 / kDownThreads;
+    constexpr int kTiles = kRows / 16, kDeep = 4 / kTiles;
     extern __shared__ __align__(16) uint8_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16, stride = F + kPad, me = static_cast<int>(threadIdx.x);
-    const int wave = uniform(me / kWave);
+    const int wave = uniform(me / kWave), half = chunk_slots * stride;
     uint8_t* codes = room;                                                      // [2][chunk_slots][F + kPad]
-    int32_t* sums = reinterpret_cast<int32_t*>(room + 2 * chunk_slots * stride);    // [S][kRows]
+    int32_t* sums = reinterpret_cast<int32_t*>(room + 2 * half);                // [S][kRows]
     f32x2* casts = reinterpret_cast<f32x2*>(sums + S * kRows);                  // [S] of a place: scale, 127 / a
     const Slots s = group_slots<kDownThreads>(topk_idx, S, E, tile_slots, reinterpret_cast<int32_t*>(casts + S));
-    const int places = uniform(s.first[s.tiles]);
-    for (int i = me; i < S * kRows; i += kDownThreads) sums[i] = 0;
-    const int n0 = static_cast<int>(blockIdx.x) * kRows, steps = F / 128, vectors = F / 4;
-    const uint32_t magic = 0xFFFFFFFFu / vectors + 1;
-    uint32_t row[kTiles];
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) row[j] = (j * 16 + i16) * static_cast<uint32_t>(F) + q * 16;
+    const int places = uniform(s.first[s.tiles]), n0 = static_cast<int>(blockIdx.x) * kRows;
 
-    // A chunk: tiles t0 .. t1 - 1, from place p0 on.  At least one tile (tile_slots <=
-    // chunk_slots).
-    struct Chunk {
-        int t0, t1, p0, p1;
-    };
-    auto chunk_from = [&](int t0) {
-        Chunk c = {t0, t0, uniform(s.first[t0]), uniform(s.first[t0])};
-        while (c.t1 < s.tiles && uniform(s.first[c.t1 + 1]) - c.p0 <= chunk_slots) c.p1 = uniform(s.first[++c.t1]);
-        return c;
-    };
-    // A chunk's h in vectors of four, thread by thread.
-    f32x4 v[kKeep];
-    auto ask_h = [&](const Chunk& c) {
-        const int all = (c.p1 - c.p0) * vectors;
-        const f32x4* from = reinterpret_cast<const f32x4*>(h + static_cast<int64_t>(c.p0) * F);
+    // Every wave meets the others once before the first chunk's cast, once behind it, and
+    // once behind each chunk but the last.
+    if (wave >= kDownWaves) {
+        constexpr int kThreads = kCastWaves * kWave, kKeep = 8;
+        const int mine = me - kDownWaves * kWave, vectors = F / 4, pieces = (vectors + kWave - 1) / kWave;
+        for (int p = mine; p < places; p += kThreads) {
+            const int columns = F / kUpOut / 4;     // in vectors of four
+            const u32x4* from = reinterpret_cast<const u32x4*>(most) + static_cast<int64_t>(p) * columns;
+            u32x4 m = {};
+            for (int c = 0; c < columns; c += 16) {
+                u32x4 v[16];
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int at = i * kDownThreads + me;
-            v[i] = from[at < all ? at : all - 1];
-        }
-    };
-    // 127 h / a by the product with 127 / a: the quotient's own error is that of fp32.
-    auto cast_h = [&](const Chunk& c, uint8_t* to) {
-        const int all = (c.p1 - c.p0) * vectors;
+                for (int e = 0; e < 16; ++e) v[e] = from[c + e < columns ? c + e : columns - 1];
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int at = i * kDownThreads + me;
-            if (at >= all) break;
-            const int p = static_cast<int>(__umulhi(at, magic));    // at / vectors: exact below 2^32 / vectors
-            const float by = casts[c.p0 + p][1];
-            uint32_t code[4];
+                for (int e = 0; e < 16; ++e)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) code[e] = __float_as_uint(__builtin_fmaf(v[i][e], by, 12582912.0f));
-            const uint32_t lo = __builtin_amdgcn_perm(code[1], code[0], 0x0C0C0400u);
-            const uint32_t hi = __builtin_amdgcn_perm(code[3], code[2], 0x04000C0Cu);
-            *reinterpret_cast<uint32_t*>(to + p * stride + (at - p * vectors) * 4) = by == 0.0f ? 0u : lo | hi;
-        }
-    };
-    u32x4 w[kDeep][kTiles][2];
-    Chunk now = chunk_from(0);
-    if (places > 0) {
-        ask_h(now);
-        if (me < places) {
-            uint32_t m = 0u;
-#pragma unroll 8
-            for (int c = 0; c < F / kUpOut; ++c) m = larger(m, most[c * S + me]);
-            const float a = __uint_as_float(m);
-            const bool none = m < 0x04000000u || m >= 0x7F800000u;     // (127 / a stays finite from 2^-119 on)
-            casts[me] = f32x2{a / 127.0f, none ? 0.0f : 127.0f * __builtin_amdgcn_rcpf(a)};
+                    for (int x = 0; x < 4; ++x) m[x] = larger(m[x], v[e][x]);
+            }
+            const uint32_t bits = larger(larger(m[0], m[1]), larger(m[2], m[3]));
+            const float a = __uint_as_float(bits);
+            const bool none = bits < 0x04000000u || bits >= 0x7F800000u;    // (127 / a stays finite from 2^-119 on)
+            casts[p] = f32x2{a / 127.0f, none ? 0.0f : 127.0f * __builtin_amdgcn_rcpf(a)};
         }
         __syncthreads();
-        cast_h(now, codes);
-    }
-    uint8_t* here = codes;
-    while (now.t0 < s.tiles) {
-        const int all = (now.t1 - now.t0) * steps, begin = all * wave / 8, end = all * (wave + 1) / 8;
-        const Chunk then = chunk_from(now.t1);
-        if (then.t0 < s.tiles) ask_h(then);
-        // The loads' tile and step.  Past its end a wave asks for its last step again.
-        int from = now.t0 + begin / steps, from_at = begin % steps, to_ask = end - begin;
-        Buffer wb;
+        // Pieces of 64 vectors of four of a place's h, place by place, every kCastWaves-th
+        // of them this wave's.  The next kKeep are asked for before these are cast.
+        struct Piece {
+            int p, i;
+        };
+        f32x4 v[2][kKeep];
+        Chunk c = chunk_from(s, 0, chunk_slots);
+        Piece asked = {wave - kDownWaves, 0};
+        auto next = [&](Piece& x) {
+            if (++x.i == pieces) {
+                x.i = 0;
+                x.p += kCastWaves;
+            }
+        };
+        // (Past a row's end the next row's, past the chunk's nothing is read.)
+        auto ask = [&](int b) {
+            const Buffer from = buffer(h + static_cast<int64_t>(c.p0) * F, static_cast<int64_t>(c.p1 - c.p0) * F * 4);
+#pragma unroll
+            for (int e = 0; e < kKeep; ++e, next(asked))
+                v[b][e] = __builtin_bit_cast(f32x4, load16(from, lane * 16, asked.p * F * 4 + asked.i * kWave * 16));
+        };
+        if (places > 0) ask(0);
+        for (int odd = 0; c.t0 < s.tiles; odd ^= 1) {
+            const int n = c.p1 - c.p0, p0 = c.p0;
+            Piece at = {wave - kDownWaves, 0};
+            auto cast = [&](int b) {
+#pragma unroll
+                for (int e = 0; e < kKeep; ++e, next(at)) {
+                    if (at.p >= n) break;
+                    const float by = casts[p0 + at.p][1];
+                    // 127 h / a by the product with 127 / a: the quotient's own error is that of fp32.
+                    uint32_t code[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) code[x] = __float_as_uint(__builtin_fmaf(v[b][e][x], by, 12582912.0f));
+                    const uint32_t lo = __builtin_amdgcn_perm(code[1], code[0], 0x0C0C0400u);
+                    const uint32_t hi = __builtin_amdgcn_perm(code[3], code[2], 0x04000C0Cu);
+                    const int vec = at.i * kWave + lane;
+                    if (vec < vectors)
+                        *reinterpret_cast<uint32_t*>(codes + odd * half + at.p * stride + vec * 4) = by == 0.0f ? 0u : lo | hi;
+                }
+            };
+            // Behind the chunk's last pieces the next chunk's first are asked for, before
+            // the waves meet.
+            do {
+                ask(1);
+                cast(0);
+                if (at.p >= n) break;
+                ask(0);
+                cast(1);
+            } while (at.p < n);
+            c = chunk_from(s, c.t1, chunk_slots);
+            asked = {wave - kDownWaves, 0};
+            if (c.t0 < s.tiles) ask(0);
+            __syncthreads();
+        }
+    } else {
+        const int steps = F / 128;
+        for (int i = me; i < S * kRows; i += kDownWaves * kWave) sums[i] = 0;
+        uint32_t row[kTiles];
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) row[j] = (j * 16 + i16) * static_cast<uint32_t>(F) + q * 16;
+        // A wave's steps of a chunk, and where they begin.
+        struct Share {
+            Chunk c;
+            int left, tile, at;
+        };
+        auto share_from = [&](int t0) {
+            Share r = {chunk_from(s, t0, chunk_slots), 0, 0, 0};
+            const int all = (r.c.t1 - r.c.t0) * steps, begin = all * wave / kDownWaves;
+            r.left = all * (wave + 1) / kDownWaves - begin;
+            r.tile = r.c.t0 + begin / steps;
+            r.at = begin % steps;
+            return r;
+        };
+        u32x4 w[kDeep][kTiles][2];
+        Share ask = share_from(0);
+        Buffer from;
         auto aim = [&] {
-            const int64_t w0 = static_cast<int64_t>(uniform(s.expert[from])) * H + n0;
-            wb = buffer(down + w0 * F, static_cast<int64_t>(kRows) * F);
+            const int64_t w0 = static_cast<int64_t>(uniform(s.expert[ask.tile])) * H + n0;
+            from = buffer(down + w0 * F, static_cast<int64_t>(kRows) * F);
+        };
+        // On to the next chunk in which the wave has a step; behind the last one its last
+        // step is asked for again.
+        auto ahead = [&] {
+            for (int t = ask.c.t1; t < s.tiles;) {
+                const Share r = share_from(t);
+                if (r.left > 0) {
+                    ask = r;
+                    aim();
+                    return;
+                }
+                t = r.c.t1;
+            }
         };
         auto load = [&](int buf) {
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) w[buf][j][half] = load16(wb, row[j], from_at * 128 + 64 * half);
+                for (int side = 0; side < 2; ++side) w[buf][j][side] = load16(from, row[j], ask.at * 128 + 64 * side);
             __builtin_amdgcn_sched_barrier(0);
-            if (--to_ask > 0 && ++from_at == steps) {
-                from_at = 0;
-                ++from;
-                aim();
+            if (ask.left > 1) {
+                --ask.left;
+                if (++ask.at == steps) {
+                    ask.at = 0;
+                    ++ask.tile;
+                    aim();
+                }
+            } else {
+                ahead();
             }
         };
-        aim();
+        Share now = ask;
+        if (places > 0) {
+            aim();
+            if (ask.left == 0) ahead();
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) load(d);
-        __syncthreads();                            // the chunk's codes are there
-        int tile = now.t0 + begin / steps, at = begin % steps, first = 0, count = 0;
-        const uint8_t* mine = here;
+            for (int d = 0; d < kDeep; ++d) load(d);
+        }
+        __syncthreads();
+        if (places > 0) __syncthreads();
+        int odd = 0, first = 0, count = 0;
+        const uint8_t* mine = codes;
         auto enter = [&] {
-            first = uniform(s.first[tile]);
-            count = uniform(s.first[tile + 1]) - first;
-            mine = here + (first - now.p0 + (i16 < count ? i16 : count - 1)) * stride + q * 16;
+            first = uniform(s.first[now.tile]);
+            count = uniform(s.first[now.tile + 1]) - first;
+            mine = codes + odd * half + (first - now.c.p0 + (i16 < count ? i16 : count - 1)) * stride + q * 16;
         };
+        // To the next chunk in which the wave has a step.
+        auto next_chunk = [&] {
+            while (now.left == 0 && now.c.t1 < s.tiles) {
+                __syncthreads();
+                odd ^= 1;
+                now = share_from(now.c.t1);
+            }
+            if (now.left > 0) enter();
+        };
+        if (places > 0 && now.left > 0) enter();
+        else next_chunk();
         i32x4 acc[kTiles] = {};
-        if (begin < end) enter();
-        for (int g = begin; g < end; g += kDeep)
+        while (now.left > 0)
 #pragma unroll
             for (int d = 0; d < kDeep; ++d) {
-                if (g + d < end) {
+                if (now.left > 0) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const u32x4 t = *reinterpret_cast<const u32x4*>(mine + at * 128 + 64 * half);
+                    for (int side = 0; side < 2; ++side) {
+                        const u32x4 t = *reinterpret_cast<const u32x4*>(mine + now.at * 128 + 64 * side);
 #pragma unroll
                         for (int j = 0; j < kTiles; ++j)
-                            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[d][j][half]),
+                            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[d][j][side]),
                                                                            __builtin_bit_cast(i32x4, t), acc[j], 0, 0, 0);
                     }
-                    if (++at == steps || g + d + 1 == end) {
+                    --now.left;
+                    if (++now.at == steps || now.left == 0) {
                         if (i16 < count) {
                             int32_t* to = sums + (first + i16) * kRows + 4 * q;
 #pragma unroll
@@ -434,35 +576,47 @@ __global__ __launch_bounds__(kDownThreads, 2) void moe_down_i8_kernel(
                         }
 #pragma unroll
                         for (int j = 0; j < kTiles; ++j) acc[j] = i32x4{};
-                        at = 0;
-                        ++tile;
-                        if (g + d + 1 < end) enter();
+                        now.at = 0;
+                        ++now.tile;
+                        if (now.left > 0) enter();
+                        else next_chunk();
                     }
                 }
                 load(d);
             }
-        // (The other half of the codes: the products of the chunk before are done.)
-        here = here == codes ? codes + chunk_slots * stride : codes;
-        if (then.t0 < s.tiles) cast_h(then, here);
-        now = then;
     }
     // Places of the slots.
     int32_t* place = reinterpret_cast<int32_t*>(codes);
-    __syncthreads();
+    __syncthreads();                                // behind the last chunk
     for (int i = me; i < S; i += kDownThreads) place[i] = -1;
     __syncthreads();
     for (int i = me; i < places; i += kDownThreads) place[s.order[i]] = i;
     __syncthreads();
+    // (Slots in batches whose loads are on the way together; those of empty slots read
+    // the first expert's scales.)
+    constexpr int kBatch = 8;
     for (int i = me; i < T * (kRows / 2); i += kDownThreads) {
         const int t = i / (kRows / 2), n = i % (kRows / 2) * 2;
         float a = 0.0f, b = 0.0f;
-        for (int j = 0; j < k; ++j) {
-            const int slot = t * k + j, p = place[slot];
-            if (p < 0) continue;
-            const float* ws = down_scales + topk_idx[slot] * H + n0 + n;
-            const float hs = casts[p][0], weight = topk_weights ? topk_weights[slot] : 1.0f;
-            a = __builtin_fmaf(weight, static_cast<float>(sums[p * kRows + n]) * (hs * ws[0]), a);
-            b = __builtin_fmaf(weight, static_cast<float>(sums[p * kRows + n + 1]) * (hs * ws[1]), b);
+        for (int j0 = 0; j0 < k; j0 += kBatch) {
+            f32x2 ws[kBatch];
+            float weight[kBatch];
+            int p[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int slot = t * k + (j0 + j < k ? j0 + j : k - 1);
+                p[j] = j0 + j < k ? place[slot] : -1;
+                const int64_t e = p[j] >= 0 ? topk_idx[slot] : 0;
+                ws[j] = *reinterpret_cast<const f32x2*>(down_scales + e * H + n0 + n);
+                weight[j] = topk_weights ? topk_weights[slot] : 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (p[j] < 0) continue;
+                const float hs = casts[p[j]][0];
+                a = __builtin_fmaf(weight[j], static_cast<float>(sums[p[j] * kRows + n]) * (hs * ws[j][0]), a);
+                b = __builtin_fmaf(weight[j], static_cast<float>(sums[p[j] * kRows + n + 1]) * (hs * ws[j][1]), b);
+            }
         }
         *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(t) * H + n0 + n) = bf16_rne(a) | bf16_rne(b) << 16;
     }
@@ -492,11 +646,11 @@ size_t moe_i8_workspace_bytes(int S, int F) {
 hipError_t launch_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int T, int k, int E, int H,
                          int F, const int8_t* up, const float* up_scales, const int8_t* down, const float* down_scales,
                          void* workspace, void* out, hipStream_t stream) {
-    const int S = T * k, rows = up_rows(H);
+    const int S = T * k, rows = up_rows(S, E, H);
     float* h = static_cast<float*>(workspace);
     uint32_t* most = reinterpret_cast<uint32_t*>(h + static_cast<int64_t>(S) * F);
     const int64_t items = static_cast<int64_t>(S) * (F / kUpOut);
-    hipLaunchKernelGGL(moe_up_i8_kernel, dim3(blocks_for(items, 512)), dim3(kUpThreads),
+    hipLaunchKernelGGL(moe_up_i8_kernel, dim3(blocks_for(items, 256)), dim3(kUpThreads),
                        static_cast<size_t>(rows) * (H + kPad) + slots_bytes(S, E), stream, static_cast<const uint16_t*>(x),
                        topk_idx, S, k, E, H, F, up, up_scales, rows, h, most);
     const hipError_t e = hipGetLastError();
