@@ -72,14 +72,14 @@ __device__ __forceinline__ f32x4 scales4(const float* scales, int n) {
 // there are not, the four waves of a block split an item's inputs, so that every CU has
 // loads in flight, and join their sums in shared memory.
 template <bool kSilu>
-__global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c, int most) {
+__global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
     constexpr int kOut = kSilu ? 32 : 64;           // outputs of an item
     constexpr int kDeep = 2;
     __shared__ i32x4 part[16][kWave];
     extern __shared__ int32_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const Table t = make_table(room, c.expert_rows, c.E, c.capacity, c.num_rows, 16, 0, most);
+    const Table t = make_table(room, c.expert_rows, c.E, c.capacity, c.num_rows, 16, 0, INT32_MAX);
     const int columns = (c.N + kOut - 1) / kOut;
     const int64_t items = static_cast<int64_t>(t.start[c.E]) * columns;
     const bool split = 4 * items < 5 * static_cast<int64_t>(gridDim.x);
@@ -412,13 +412,13 @@ __device__ __forceinline__ void tile_item(const Call& c, const Item& it, const F
 }
 
 template <bool kSilu>
-__global__ __launch_bounds__(kThreads, 1) void tile_i8_kernel(Call c, int above) {
+__global__ __launch_bounds__(kThreads, 1) void tile_i8_kernel(Call c) {
     constexpr int kOut = kSilu ? kTileWeights8 / 2 : kTileWeights8;
     __shared__ __align__(1024) uint8_t ring[2 * kSlot];
     // Of an item's weight rows and token rows; the next item's come to the other.
     __shared__ __align__(16) float scales[2][kTileWeights8 + kTileRows8];
     extern __shared__ int32_t room[];
-    const Table t = make_table(room, c.expert_rows, c.E, c.capacity, c.num_rows, kTileRows8, above, INT32_MAX);
+    const Table t = make_table(room, c.expert_rows, c.E, c.capacity, c.num_rows, kTileRows8, 0, INT32_MAX);
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave), lane = lane_id();
     const int columns = (c.N + kOut - 1) / kOut, stages = c.K / kStage;
     const Share mine = share_of(static_cast<int64_t>(t.start[c.E]) * columns);
@@ -468,18 +468,11 @@ int64_t most_tiles(const Call& c, int rows) { return c.num_rows / rows + (c.num_
 
 template <bool kSilu>
 hipError_t launch(const Call& c, hipStream_t stream) {
-    const I8Plan plan = i8_plan(c.num_rows, c.capacity, c.E);
-    if (plan.stream_most > 0) {
-        const int64_t items = most_tiles(c, 16) * ceil_div(c.N, kSilu ? 32 : 64);
-        hipLaunchKernelGGL((stream_i8_kernel<kSilu>), dim3(blocks_for(items, 256 * 2)), dim3(kThreads),
-                           table_bytes(c.E), stream, c, plan.stream_most);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    if (plan.tile_above == INT32_MAX) return hipSuccess;
-    const int64_t items = most_tiles(c, kTileRows8) * ceil_div(c.N, kSilu ? kTileWeights8 / 2 : kTileWeights8);
-    hipLaunchKernelGGL((tile_i8_kernel<kSilu>), dim3(blocks_for(items, 256)), dim3(kThreads), table_bytes(c.E), stream,
-                       c, plan.tile_above);
+    const bool streams = i8_streams(c.num_rows, c.E, c.K, c.N, kSilu);
+    const int64_t items = streams ? most_tiles(c, 16) * ceil_div(c.N, kSilu ? 32 : 64)
+                                  : most_tiles(c, kTileRows8) * ceil_div(c.N, kSilu ? kTileWeights8 / 2 : kTileWeights8);
+    hipLaunchKernelGGL(streams ? stream_i8_kernel<kSilu> : tile_i8_kernel<kSilu>,
+                       dim3(blocks_for(items, streams ? 256 * 2 : 256)), dim3(kThreads), table_bytes(c.E), stream, c);
     return hipGetLastError();
 }
 

@@ -10,20 +10,23 @@ namespace ep {
 // Token rows of a full tile, and its weight rows.
 constexpr int kTileRows8 = 256, kTileWeights8 = 256;
 
-// Rows of an expert up to which its weights are streamed.
-constexpr int kFew8 = 16;
-
-// Each launch takes the experts that suit it, as their rows are known on the device
-// only; one is left out where it would find none or few.
-struct I8Plan {
-    int stream_most;                                // experts of up to so many rows (0: no launch)
-    int tile_above;                                 // experts of more rows than this (INT32_MAX: no launch)
-};
-constexpr I8Plan i8_plan(int64_t num_rows, int capacity, int E) {
-    const int64_t most = capacity > 0 ? capacity : num_rows, mean = num_rows / E;
-    const bool both = capacity > 0 || mean <= 2 * kFew8;
-    if (both && most <= kFew8) return {kFew8, INT32_MAX};
-    return both ? I8Plan{kFew8, kFew8} : I8Plan{0, 0};
+// A call launches one kernel, for all of its experts: streams (16 token rows x 64 weight
+// rows a wave or block) where they all find room on the card at once, for tiles have a
+// quarter of the items at most and leave CUs without one; but not over few inputs, where
+// a tile's time is short.  Streams against tiles (us), by items as counted here: 96,
+// 64 experts with 6 rows, 4096 -> 2 x 1024, 14 / 28; 256, 256 with 8, 7168 -> 2 x 2048,
+// 46 / 65; 256, 16 with 128, 1024 -> 1024, 9 / 13; 512, 8 with 64, 4096 -> 4096, 28 / 34;
+// 576, 256 with 16, 7168 -> 2 x 2048, 82 / 85; but 448, 256 with 8, 2048 -> 7168, 25.4 /
+// 24.7; 768, 8 with 128, 4096 -> 4096, 44 / 35; 272, 60 with 64, 512 -> 512, 12 / 11.
+// (However few rows the experts have, tiles are as fast where there are enough of them:
+// 256 experts of 4 rows, 2048 -> 7168, 655 / 634; of 16, 1074 / 685.)
+// The rows of a padded call are those of its buffer, however few are filled.
+constexpr int64_t kStreamItems8 = 640;
+constexpr int kStreamInputs8 = 1024;
+constexpr bool i8_streams(int64_t num_rows, int E, int K, int N, bool silu) {
+    const int64_t halves = (num_rows < E ? num_rows : E) / 2;       // of an expert's last tile, on average
+    const int64_t columns = (N + (silu ? 31 : 63)) / (silu ? 32 : 64);
+    return K >= kStreamInputs8 && (num_rows / 16 + halves) * columns <= kStreamItems8;
 }
 
 // ---- the stages of a tile ------------------------------------------------------------

@@ -15,9 +15,8 @@ extern "C" void quarter(int q, int* out) {
     const ep::I8Quarter s = ep::i8_quarter(q);
     out[0] = s.from; out[1] = s.to; out[2] = s.later; out[3] = s.early;
 }
-extern "C" void plan(long long num_rows, int capacity, int E, int* out) {
-    const ep::I8Plan p = ep::i8_plan(num_rows, capacity, E);
-    out[0] = p.stream_most; out[1] = p.tile_above;
+extern "C" int streams(long long num_rows, int E, int K, int N, int silu) {
+    return ep::i8_streams(num_rows, E, K, N, silu != 0);
 }
 """
 
@@ -37,3 +36,8 @@ def quarter(q):
     out = (ctypes.c_int * 4)()
     lib().quarter(q, out)
     return tuple(out)
+
+
+def way(num_rows, E, K, N, silu):
+    """What a call launches: "streams" or "tiles"."""
+    return "streams" if lib().streams(ctypes.c_longlong(num_rows), E, K, N, int(silu)) else "tiles"
