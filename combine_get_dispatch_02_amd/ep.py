@@ -142,15 +142,21 @@ def _check_out(out: Dict[str, Optional[torch.Tensor]], dev: torch.device, spec) 
     """Caller-supplied outputs: spec rows are (name, shape, dtype, required,
     capacity).  A capacity buffer needs at least shape[0] rows and exactly the
     trailing shape; any other array needs exactly `shape`.  The kernels write
-    through raw pointers, so a smaller or mistyped tensor is refused here."""
+    through raw pointers, so a smaller or mistyped tensor is refused here.
+    (What is in order is seen by a few comparisons: small calls pay for each.)"""
+    index = dev.index
     for name, shape, dtype, required, capacity in spec:
         t = out.get(name)
         if t is None:
             if required:
                 raise ValueError(f"out is missing {name}")
             continue
-        _need(t, name, dtype, dev)
-        got = tuple(t.shape)
+        got = t.shape
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            _need(t, name, dtype, dev)
+        if got == shape:
+            continue
+        got = tuple(got)
         ok = (len(got) == len(shape) and got[0] >= shape[0] and got[1:] == tuple(shape[1:])) if capacity \
             else got == tuple(shape)
         if not ok:
@@ -725,7 +731,11 @@ def _need_tokens(fn: str, x: torch.Tensor, slots: torch.Tensor, dtype: torch.dty
     xs, ks = x.shape, slots.shape
     if len(xs) != 2 or len(ks) != 2 or ks[0] != xs[0]:
         raise ValueError(f"{fn}: x must be [T, H], topk_idx (or token_row) [T, k]")
-    _need_int32(fn, hidden=xs[1], num_topk=ks[1], **values)
+    high = xs[1] | ks[1]
+    for v in values.values():
+        high |= v
+    if high >> 31:
+        _need_int32(fn, hidden=xs[1], num_topk=ks[1], **values)
     _need(x, "x", torch.bfloat16)
     _need(slots, "topk_idx" if dtype is torch.int64 else "token_row", dtype, x.device)
     if weights is not None:
@@ -814,7 +824,8 @@ def ep_quantize_i8(x: torch.Tensor, expert_rows: Optional[torch.Tensor] = None, 
     shape = x.shape
     if len(shape) not in ((2, 3) if capacity else (2,)):
         raise ValueError("x must be [rows, K] (or [E, capacity, K])")
-    _need_int32("ep_quantize_i8", capacity=capacity, hidden=shape[-1])
+    if (capacity | shape[-1]) >> 31:
+        _need_int32("ep_quantize_i8", capacity=capacity, hidden=shape[-1])
     _need(x, "x", torch.bfloat16)
     dev = x.device
     E = 0
@@ -832,8 +843,7 @@ def ep_quantize_i8(x: torch.Tensor, expert_rows: Optional[torch.Tensor] = None, 
         out = dict(x_i8=torch.empty(shape, dtype=torch.int8, device=dev),
                    x_scales=torch.empty(shape[:-1], dtype=torch.float32, device=dev))
     else:
-        _check_out(out, dev, [("x_i8", tuple(shape), torch.int8, True, False),
-                              ("x_scales", tuple(shape[:-1]), torch.float32, True, False)])
+        _check_out(out, dev, (("x_i8", shape, torch.int8, True, False), ("x_scales", shape[:-1], torch.float32, True, False)))
     rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
     _launch("ep_quantize_i8", dev, x.data_ptr(), rows, shape[-1], _addr(expert_rows), E, capacity,
             out["x_i8"].data_ptr(), out["x_scales"].data_ptr())
