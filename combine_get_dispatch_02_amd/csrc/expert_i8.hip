@@ -227,15 +227,30 @@ struct Item {
     int e, left, n0;                                // expert, token rows, first output
     int64_t row0;
 };
+// A block's items one after the other, by tile and column: `tiles` and `columns` on to
+// the next one, without a division.
+struct Walk {
+    int64_t left;                                   // items, this one among them
+    int tile, column;
+    int tiles, columns, all;                        // step; columns of a tile
+    __device__ __forceinline__ void on() {
+        --left;
+        tile += tiles;
+        column += columns;
+        if (column >= all) {
+            column -= all;
+            ++tile;
+        }
+    }
+};
 // An expert's rows go to its tiles in equal parts, of whole 64: four tiles of 192 rows
 // end together, three of 256 and one of 10 do not.
-__device__ __forceinline__ Item item_of(const Table& t, int E, int64_t item, int columns, int outputs) {
-    const int tile = static_cast<int>(item / columns), e = expert_of(t, E, tile);
-    const int count = __builtin_amdgcn_readfirstlane(t.count[e]);
-    const int tiles = (count - 1) / kTileRows8 + 1, rows = ((count - 1) / tiles / 64 + 1) * 64;
-    const int m0 = (tile - __builtin_amdgcn_readfirstlane(t.start[e])) * rows;
-    return {e, count - m0 < rows ? count - m0 : rows,
-            static_cast<int>(item - static_cast<int64_t>(tile) * columns) * outputs,
+__device__ __forceinline__ Item item_of(const Table& t, int E, const Walk& w, int outputs) {
+    const int e = expert_of(t, E, w.tile), count = __builtin_amdgcn_readfirstlane(t.count[e]);
+    const uint32_t tiles = (count - 1) / kTileRows8 + 1;
+    const int rows = (static_cast<uint32_t>(count - 1) / tiles / 64 + 1) * 64;
+    const int m0 = (w.tile - __builtin_amdgcn_readfirstlane(t.start[e])) * rows;
+    return {e, count - m0 < rows ? count - m0 : rows, w.column * outputs,
             __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0)};
 }
 
@@ -424,16 +439,22 @@ __global__ __launch_bounds__(kThreads, 1) void tile_i8_kernel(Call c) {
     const Share mine = share_of(static_cast<int64_t>(t.start[c.E]) * columns);
     if (mine.at >= mine.end) return;
     const uint32_t at_ring = shared_at(ring);
+    const int step = static_cast<int>(mine.step), first = static_cast<int>(mine.at / columns);
+    Walk walk = {(mine.end - mine.at - 1) / mine.step + 1, first,
+                 static_cast<int>(mine.at - static_cast<int64_t>(first) * columns), step / columns, step % columns, columns};
 
     Fill f;
-    int64_t filling = mine.at;
-    aim<kSilu>(f, c, item_of(t, c.E, filling, columns, kOut), wave);
+    Walk filling = walk;
+    aim<kSilu>(f, c, item_of(t, c.E, filling, kOut), wave);
     // Behind the last item its last stage is asked for again.
     auto advance = [&] {
         if (++f.stage < stages) return;
-        filling += mine.step;
-        if (filling < mine.end) aim<kSilu>(f, c, item_of(t, c.E, filling, columns, kOut), wave);
-        else f.stage = stages - 1;
+        if (filling.left > 1) {
+            filling.on();
+            aim<kSilu>(f, c, item_of(t, c.E, filling, kOut), wave);
+        } else {
+            f.stage = stages - 1;
+        }
     };
 #pragma unroll
     for (int d = 0; d < 2; ++d) {
@@ -444,8 +465,8 @@ __global__ __launch_bounds__(kThreads, 1) void tile_i8_kernel(Call c) {
     arrive<kLoads>();
     uint32_t here = 0;
     int odd = 0, stored = 0;                        // stores of the last item
-    for (int64_t item = mine.at; item < mine.end; item += mine.step, odd ^= 1) {
-        const Item it = item_of(t, c.E, item, columns, kOut);
+    for (; walk.left > 0; walk.on(), odd ^= 1) {
+        const Item it = item_of(t, c.E, walk, kOut);
         const int wide = c.N - it.n0 < kTileWeights8 ? c.N - it.n0 : kTileWeights8;
         // Scales in the order of the slot's rows.
         const int64_t w0 = static_cast<int64_t>(it.e) * (kSilu ? 2 * c.N : c.N) + it.n0 + (kSilu && wave % 2 == 1 ? c.N : 0);
