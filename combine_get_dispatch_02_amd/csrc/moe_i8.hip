@@ -161,44 +161,58 @@ constexpr int kPad = 16;
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // ---- up ------------------------------------------------------------------------------
-// A block takes a run of items: 32 gate rows and their 32 up rows of an expert against
-// a tile of its slots.  Its eight waves split an item's inputs and join their sums in
-// shared memory; their loads run on from one item to the next.  The tokens of a tile
-// are cast into shared memory when its first item comes.
+// An item is 32 gate rows and their 32 up rows of an expert against a tile of its slots.
+// A block's eight waves take a run of items together, splitting each item's inputs and
+// joining their sums in shared memory; or (kAlone), where there are few inputs to split,
+// each wave takes a run of its own, and no wave waits for another.  Loads run on from one item to the next.  The tokens of a tile are cast into
+// shared memory when its first item comes.
 constexpr int kUpThreads = 512, kUpWaves = kUpThreads / kWave, kUpDeep = 2;
 constexpr int kUpShared = 126 * 1024;               // bytes of a CU's 160 KB beside what is declared below
 constexpr int kUpOut = 32;                          // outputs of an item
 
 // Rows of a tile: as many as find room.
-int up_rows(int S, int E, int H) {
-    const int rows = (kUpShared - static_cast<int>(slots_bytes(S, E))) / (H + kPad);
+int up_rows(int S, int E, int H, bool alone) {
+    const int rows = (kUpShared - static_cast<int>(slots_bytes(S, E))) / (H + kPad) / (alone ? kUpWaves : 1);
     return rows < 16 ? rows : 16;
 }
 
-// The largest |h| of a place's outputs of one item, as fp32 bits: at most[place * (F /
-// 32) + column].
+// What a wave wrote to shared memory is there for its other lanes.
+__device__ __forceinline__ void settle_wave() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The largest |h| of a slot's outputs of one item, as fp32 bits: at most[slot * (F / 32)
+// + column].
+template <bool kAlone>
 __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t* __restrict__ x,
                                                                   const int64_t* __restrict__ topk_idx, int S, int k,
                                                                   int E, int H, int F, const int8_t* __restrict__ up,
                                                                   const float* __restrict__ up_scales, int rows,
                                                                   float* __restrict__ h, uint32_t* __restrict__ most) {
-    constexpr int kBatch = 4;                       // rows cast at a time
-    __shared__ i32x4 part[kUpWaves][4][kWave];
-    __shared__ float x_scale[16];
-    __shared__ uint32_t row_room[2][kBatch][kUpThreads / kWave], h_room[16];
+    constexpr int kTeam = kAlone ? 1 : kUpWaves;    // waves that share an item
+    constexpr int kThreads = kTeam * kWave, kBatch = kAlone ? 2 : 4;        // (rows cast at a time)
+    constexpr int kSides = kAlone ? 2 : 1;          // groups of 16 outputs that a wave finishes
+    __shared__ i32x4 part[kAlone ? 1 : kUpWaves][4][kWave];
+    __shared__ float x_scale[kUpWaves / kTeam][16];
+    __shared__ uint32_t row_room[2][kBatch][kTeam], h_room[16];
     extern __shared__ __align__(16) uint8_t room[];
-    uint8_t* codes = room;                          // [rows][H + kPad]
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16, stride = H + kPad;
-    const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
-    const Slots s = group_slots<kUpThreads>(topk_idx, S, E, rows, reinterpret_cast<int32_t*>(room + rows * stride));
+    const int block_wave = uniform(static_cast<int>(threadIdx.x) / kWave), wave = kAlone ? 0 : block_wave;
+    const int team = kAlone ? block_wave : 0, me = wave * kWave + lane;
+    uint8_t* codes = room + team * rows * stride;   // [rows][H + kPad]
+    const Slots s = group_slots<kUpThreads>(topk_idx, S, E, rows,
+                                            reinterpret_cast<int32_t*>(room + kUpWaves / kTeam * rows * stride));
     const int columns = F / kUpOut;
     const int64_t items = static_cast<int64_t>(s.tiles) * columns;
     // Blocks go to the 8 chiplets in turn: neighbouring runs to the blocks of one.
-    const int64_t b = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
-    const int64_t begin = items * b / gridDim.x, end = items * (b + 1) / gridDim.x;
+    const int64_t b = (blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8) * (kUpWaves / kTeam) + team;
+    const int64_t runs = static_cast<int64_t>(gridDim.x) * (kUpWaves / kTeam);
+    const int64_t begin = items * b / runs, end = items * (b + 1) / runs;
     if (begin == end) return;
-    // A wave's steps of an item: inputs 128 (wave + 8 i) .. + 127.
-    const int steps = (H / 128 + kUpWaves - 1) / kUpWaves;
+    // A wave's steps of an item: inputs 128 (wave + kTeam i) .. + 127.
+    const int steps = (H / 128 + kTeam - 1) / kTeam;
 
     // The loading side.  Past its end a wave asks for its last step again.
     u32x4 w[kUpDeep][4][2];
@@ -215,7 +229,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
         from[1] = buffer(p + static_cast<int64_t>(F) * H, static_cast<int64_t>(kUpOut) * H);
     };
     auto load = [&](int buf) {
-        int at = (wave + ask_step * kUpWaves) * 128;
+        int at = (wave + ask_step * kTeam) * 128;
         at = at < H ? at : H - 128;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -244,13 +258,13 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
             const int token = uniform(s.order[first + (r0 + r < count ? r0 + r : count - 1)]) / k;
             from_x[r] = reinterpret_cast<const u32x4*>(x + static_cast<int64_t>(token) * H);
         }
-        cast_rows<kUpThreads, 1, kBatch>(
-            from_x, H / 16, static_cast<int>(threadIdx.x), row_room[r0 / kBatch % 2], ready,
+        cast_rows<kThreads, kAlone ? 2 : 1, kBatch>(
+            from_x, H / 16, me, row_room[r0 / kBatch % 2], ready,
             [&](int r, int p, const u32x4& v) {
                 if (r0 + r < count) *reinterpret_cast<u32x4*>(codes + (r0 + r) * stride + p * 16) = v;
             },
             [&](int r, float scale) {
-                if (threadIdx.x == 0 && r0 + r < count) x_scale[r0 + r] = scale;
+                if (me == 0 && r0 + r < count) x_scale[team][r0 + r] = scale;
             });
     };
     auto stage = [&](int now, auto ready) {
@@ -260,49 +274,64 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
         cast_batch(0, ready);
         for (int r0 = kBatch; r0 < count; r0 += kBatch) cast_batch(r0, [] {});
         mine = codes + (i16 < count ? i16 : count - 1) * stride + q * 16;
-        __syncthreads();
+        if constexpr (kAlone) settle_wave();
+        else __syncthreads();
     };
 
     i32x4 acc[4] = {};
     // The scales of an item's rows, asked for while the item before is finished.
-    f32x4 gs, us;
+    f32x4 gs[kSides], us[kSides];
     auto ask_scales = [&](int64_t item) {
         const int t = static_cast<int>(item / columns), column = static_cast<int>(item - static_cast<int64_t>(t) * columns);
         const float* ws = up_scales + static_cast<int64_t>(uniform(s.expert[t])) * 2 * F + column * kUpOut + wave % 2 * 16 + 4 * q;
-        gs = *reinterpret_cast<const f32x4*>(ws);
-        us = *reinterpret_cast<const f32x4*>(ws + F);
+#pragma unroll
+        for (int g = 0; g < kSides; ++g) {
+            gs[g] = *reinterpret_cast<const f32x4*>(ws + g * 16);
+            us[g] = *reinterpret_cast<const f32x4*>(ws + F + g * 16);
+        }
+    };
+    // Four outputs of the lane's slot, from n on, and their largest magnitude so far.
+    auto result = [&](const i32x4& gate, const i32x4& other, int g, int n, uint32_t m) {
+        const float xs = x_scale[team][i16];
+        f32x4 v;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            v[c] = silu(static_cast<float>(gate[c]) * (xs * gs[g][c])) * (static_cast<float>(other[c]) * (xs * us[g][c]));
+            m = larger(m, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+        }
+        *reinterpret_cast<f32x4*>(h + static_cast<int64_t>(s.order[first + i16]) * F + n) = v;
+        return m;
     };
     // The waves' sums of an item, and its results.
     auto finish = [&](int column) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            part[wave][j][lane] = acc[j];
-            acc[j] = i32x4{};
-        }
-        __syncthreads();
         uint32_t m = 0u;
-        if (wave < 2 && i16 < count) {
-            auto sum = [&](int j) {
-                i32x4 v = part[0][j][lane];
+        if constexpr (kAlone) {
+            if (i16 < count)
 #pragma unroll
-                for (int o = 1; o < kUpWaves; ++o) v += part[o][j][lane];
-                return v;
-            };
-            const int n = column * kUpOut + wave * 16 + 4 * q;
-            const i32x4 gate = sum(wave), other = sum(wave + 2);
-            const float xs = x_scale[i16];
-            f32x4 v;
+                for (int g = 0; g < 2; ++g) m = result(acc[g], acc[g + 2], g, column * kUpOut + g * 16 + 4 * q, m);
+            m = across_rows(m);
+            if (lane < count) most[static_cast<int64_t>(s.order[first + lane]) * columns + column] = m;
+        } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                v[c] = silu(static_cast<float>(gate[c]) * (xs * gs[c])) * (static_cast<float>(other[c]) * (xs * us[c]));
-                m = larger(m, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+            for (int j = 0; j < 4; ++j) part[wave][j][lane] = acc[j];
+            __syncthreads();
+            if (wave < 2 && i16 < count) {
+                auto sum = [&](int j) {
+                    i32x4 v = part[0][j][lane];
+#pragma unroll
+                    for (int o = 1; o < kTeam; ++o) v += part[o][j][lane];
+                    return v;
+                };
+                m = result(sum(wave), sum(wave + 2), 0, column * kUpOut + wave * 16 + 4 * q, m);
             }
-            *reinterpret_cast<f32x4*>(h + static_cast<int64_t>(first + i16) * F + n) = v;
+            m = across_rows(m);
+            if (wave == 1 && q == 0) h_room[i16] = m;
+            __syncthreads();
+            if (wave == 0 && lane < count)
+                most[static_cast<int64_t>(s.order[first + lane]) * columns + column] = larger(m, h_room[lane]);
         }
-        m = across_rows(m);
-        if (wave == 1 && q == 0) h_room[i16] = m;
-        __syncthreads();
-        if (wave == 0 && lane < count) most[(first + lane) * static_cast<int64_t>(columns) + column] = larger(m, h_room[lane]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = i32x4{};
     };
 
     aim();
@@ -320,9 +349,10 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
             if (g + d < total) {
                 if (step == 0 && column == columns) {
                     column = 0;
+                    if constexpr (kAlone) settle_wave();    // the last tile's codes are read
                     stage(tile + 1, [] {});
                 }
-                const int at = (wave + step * kUpWaves) * 128;
+                const int at = (wave + step * kTeam) * 128;
                 if (at < H) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -344,8 +374,10 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
 }
 
 // ---- down ----------------------------------------------------------------------------
-// A block has kRows outputs of every token.  It takes the slots in chunks whose codes fit
-// half of its shared memory for them.  Eight waves multiply: a chunk's products, tile
+// A block has kRows outputs of every token, or of a part of the tokens where that leaves
+// CUs without a block (the experts that two parts have in common are read twice, but
+// mostly out of the caches).  It takes the slots in chunks whose codes fit half of its
+// shared memory for them.  Eight waves multiply: a chunk's products, tile
 // after tile and 128 inputs at a time, are one row of steps of which each takes an
 // eighth; their loads run on from one chunk to the next, and sums meet in shared memory
 // by integer additions.  Eight more waves cast the next chunk's h meanwhile.  (The same
@@ -377,17 +409,29 @@ __device__ __forceinline__ Chunk chunk_from(const Slots& s, int t0, int slots) {
 template <int kRows>
 __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_kernel(
     const float* __restrict__ h, const uint32_t* __restrict__ most, const int64_t* __restrict__ topk_idx,
-    const float* __restrict__ topk_weights, int S, int T, int k, int E, int H, int F, const int8_t* __restrict__ down,
-    const float* __restrict__ down_scales, int chunk_slots, int tile_slots, uint16_t* __restrict__ out) {
+    const float* __restrict__ topk_weights, int T, int parts, int k, int E, int H, int F,
+    const int8_t* __restrict__ down, const float* __restrict__ down_scales, int chunk_slots, int tile_slots,
+    uint16_t* __restrict__ out) {
     constexpr int kTiles = kRows / 16, kDeep = 4 / kTiles;
     extern __shared__ __align__(16) uint8_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16, stride = F + kPad, me = static_cast<int>(threadIdx.x);
     const int wave = uniform(me / kWave), half = chunk_slots * stride;
+    // From here on tokens, slots and what belongs to them are those of the block's part.
+    const int part = static_cast<int>(blockIdx.x) / (H / kRows), n0 = static_cast<int>(blockIdx.x) % (H / kRows) * kRows;
+    const int token0 = static_cast<int>(static_cast<int64_t>(T) * part / parts);
+    T = static_cast<int>(static_cast<int64_t>(T) * (part + 1) / parts) - token0;
+    const int S = T * k;
+    const int64_t slot0 = static_cast<int64_t>(token0) * k;
+    topk_idx += slot0;
+    if (topk_weights) topk_weights += slot0;
+    h += slot0 * F;
+    most += slot0 * (F / kUpOut);
+    out += static_cast<int64_t>(token0) * H;
     uint8_t* codes = room;                                                      // [2][chunk_slots][F + kPad]
     int32_t* sums = reinterpret_cast<int32_t*>(room + 2 * half);                // [S][kRows]
     f32x2* casts = reinterpret_cast<f32x2*>(sums + S * kRows);                  // [S] of a place: scale, 127 / a
     const Slots s = group_slots<kDownThreads>(topk_idx, S, E, tile_slots, reinterpret_cast<int32_t*>(casts + S));
-    const int places = uniform(s.first[s.tiles]), n0 = static_cast<int>(blockIdx.x) * kRows;
+    const int places = uniform(s.first[s.tiles]);
 
     // Every wave meets the others once before the first chunk's cast, once behind it, and
     // once behind each chunk but the last.
@@ -396,7 +440,7 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
         const int mine = me - kDownWaves * kWave, vectors = F / 4, pieces = (vectors + kWave - 1) / kWave;
         for (int p = mine; p < places; p += kThreads) {
             const int columns = F / kUpOut / 4;     // in vectors of four
-            const u32x4* from = reinterpret_cast<const u32x4*>(most) + static_cast<int64_t>(p) * columns;
+            const u32x4* from = reinterpret_cast<const u32x4*>(most) + static_cast<int64_t>(s.order[p]) * columns;
             u32x4 m = {};
             for (int c = 0; c < columns; c += 16) {
                 u32x4 v[16];
@@ -416,31 +460,31 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
         // Pieces of 64 vectors of four of a place's h, place by place, every kCastWaves-th
         // of them this wave's.  The next kKeep are asked for before these are cast.
         struct Piece {
-            int p, i;
+            int p, i, row;
         };
         f32x4 v[2][kKeep];
         Chunk c = chunk_from(s, 0, chunk_slots);
-        Piece asked = {wave - kDownWaves, 0};
-        auto next = [&](Piece& x) {
-            if (++x.i == pieces) {
-                x.i = 0;
-                x.p += kCastWaves;
+        const Buffer from = buffer(h, static_cast<int64_t>(S) * F * 4);
+        Piece asked = {};
+        auto begin = [&](Piece& x, int p) {
+            x = {p, 0, p < c.p1 - c.p0 ? uniform(s.order[c.p0 + p]) : S};
+        };
+        // (Past a row's end the next row's are read, past the chunk's last row nothing.)
+        auto ask = [&](int b) {
+#pragma unroll
+            for (int e = 0; e < kKeep; ++e) {
+                v[b][e] = __builtin_bit_cast(f32x4, load16(from, lane * 16, asked.row * F * 4 + asked.i * kWave * 16));
+                if (++asked.i == pieces) begin(asked, asked.p + kCastWaves);
             }
         };
-        // (Past a row's end the next row's, past the chunk's nothing is read.)
-        auto ask = [&](int b) {
-            const Buffer from = buffer(h + static_cast<int64_t>(c.p0) * F, static_cast<int64_t>(c.p1 - c.p0) * F * 4);
-#pragma unroll
-            for (int e = 0; e < kKeep; ++e, next(asked))
-                v[b][e] = __builtin_bit_cast(f32x4, load16(from, lane * 16, asked.p * F * 4 + asked.i * kWave * 16));
-        };
+        begin(asked, wave - kDownWaves);
         if (places > 0) ask(0);
         for (int odd = 0; c.t0 < s.tiles; odd ^= 1) {
             const int n = c.p1 - c.p0, p0 = c.p0;
-            Piece at = {wave - kDownWaves, 0};
+            Piece at = {wave - kDownWaves, 0, 0};
             auto cast = [&](int b) {
 #pragma unroll
-                for (int e = 0; e < kKeep; ++e, next(at)) {
+                for (int e = 0; e < kKeep; ++e) {
                     if (at.p >= n) break;
                     const float by = casts[p0 + at.p][1];
                     // 127 h / a by the product with 127 / a: the quotient's own error is that of fp32.
@@ -452,6 +496,10 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
                     const int vec = at.i * kWave + lane;
                     if (vec < vectors)
                         *reinterpret_cast<uint32_t*>(codes + odd * half + at.p * stride + vec * 4) = by == 0.0f ? 0u : lo | hi;
+                    if (++at.i == pieces) {
+                        at.i = 0;
+                        at.p += kCastWaves;
+                    }
                 }
             };
             // Behind the chunk's last pieces the next chunk's first are asked for, before
@@ -464,7 +512,7 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
                 cast(1);
             } while (at.p < n);
             c = chunk_from(s, c.t1, chunk_slots);
-            asked = {wave - kDownWaves, 0};
+            begin(asked, wave - kDownWaves);
             if (c.t0 < s.tiles) ask(0);
             __syncthreads();
         }
@@ -622,18 +670,54 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
     }
 }
 
+struct Call {
+    const void* x;
+    const int64_t* topk_idx;
+    const float* topk_weights;
+    int T, k, E, H, F;
+    const int8_t* up;
+    const float* up_scales;
+    const int8_t* down;
+    const float* down_scales;
+    float* h;
+    uint32_t* most;
+    void* out;
+    hipStream_t stream;
+};
+
+// Below so many inputs each wave takes items by itself: an eighth of them is two steps
+// at most, and joining eight waves' sums costs more.  Alone against together (us, both
+// launches): 1 token, 8 of 256, 1024 -> 2048, 29 / 34; 30 tokens, 6 of 128, 384 -> 1408,
+// 54 / 77; 64, 8 of 256, 1792 -> 768, 211 / 220; but 64, 8 of 8, 1024 -> 2048, 85 / 79; 1,
+// 8 of 64, 2048 -> 768, 29 / 28; 16, 6 of 64, 2048 -> 1408, 113 / 111; 64, 6 of 64, 4096 ->
+// 1024, 300 / 192.
+constexpr int kTogether = 2048;
+
+template <bool kAlone>
+hipError_t launch_up(const Call& c) {
+    const int S = c.T * c.k, rows = up_rows(S, c.E, c.H, kAlone);
+    const int64_t items = static_cast<int64_t>(S) * (c.F / kUpOut);
+    hipLaunchKernelGGL((moe_up_i8_kernel<kAlone>), dim3(blocks_for(items, 256)), dim3(kUpThreads),
+                       static_cast<size_t>(rows) * (c.H + kPad) * (kAlone ? kUpWaves : 1) + slots_bytes(S, c.E), c.stream,
+                       static_cast<const uint16_t*>(c.x), c.topk_idx, S, c.k, c.E, c.H, c.F, c.up, c.up_scales, rows, c.h,
+                       c.most);
+    return hipGetLastError();
+}
+
 template <int kRows>
-hipError_t launch_down(const float* h, const uint32_t* most, const int64_t* topk_idx, const float* topk_weights, int T,
-                       int k, int E, int H, int F, const int8_t* down, const float* down_scales, void* out,
-                       hipStream_t stream) {
-    const int S = T * k, stride = F + kPad;
+hipError_t launch_down(const Call& c) {
+    // Parts of the tokens where a quarter of the CUs or more would have no block.  (Both
+    // launches, one part against as many as this: 30 tokens, 6 of 128 experts, 384 -> 1408,
+    // 147 / 77 us; 64, 4 of 64, 1024 -> 768, 82 / 63; 64, 8 of 256, 2048 -> 768, 260 / 231.)
+    const int blocks = c.H / kRows, most_parts = blocks >= 192 ? 1 : 256 / blocks, parts = most_parts < c.T ? most_parts : c.T;
+    const int S = (c.T + parts - 1) / parts * c.k, stride = c.F + kPad;
     static_assert(kMoeMaxFfn <= kDownCodes, "a slot's codes fit");
-    int chunk = kDownCodes / F < kDownRoom / stride ? kDownCodes / F : kDownRoom / stride;
+    int chunk = kDownCodes / c.F < kDownRoom / stride ? kDownCodes / c.F : kDownRoom / stride;
     if (chunk > S) chunk = S;
-    const size_t lds = 2 * static_cast<size_t>(chunk) * stride + sizeof(int32_t) * S * kRows + sizeof(f32x2) * S + slots_bytes(S, E);
-    hipLaunchKernelGGL((moe_down_i8_kernel<kRows>), dim3(static_cast<unsigned>(H / kRows)), dim3(kDownThreads), lds,
-                       stream, h, most, topk_idx, topk_weights, S, T, k, E, H, F, down, down_scales, chunk,
-                       chunk < 16 ? chunk : 16, static_cast<uint16_t*>(out));
+    const size_t lds = 2 * static_cast<size_t>(chunk) * stride + sizeof(int32_t) * S * kRows + sizeof(f32x2) * S + slots_bytes(S, c.E);
+    hipLaunchKernelGGL((moe_down_i8_kernel<kRows>), dim3(static_cast<unsigned>(blocks * parts)), dim3(kDownThreads), lds,
+                       c.stream, c.h, c.most, c.topk_idx, c.topk_weights, c.T, parts, c.k, c.E, c.H, c.F, c.down,
+                       c.down_scales, chunk, chunk < 16 ? chunk : 16, static_cast<uint16_t*>(c.out));
     return hipGetLastError();
 }
 
@@ -646,18 +730,12 @@ size_t moe_i8_workspace_bytes(int S, int F) {
 hipError_t launch_moe_i8(const void* x, const int64_t* topk_idx, const float* topk_weights, int T, int k, int E, int H,
                          int F, const int8_t* up, const float* up_scales, const int8_t* down, const float* down_scales,
                          void* workspace, void* out, hipStream_t stream) {
-    const int S = T * k, rows = up_rows(S, E, H);
     float* h = static_cast<float*>(workspace);
-    uint32_t* most = reinterpret_cast<uint32_t*>(h + static_cast<int64_t>(S) * F);
-    const int64_t items = static_cast<int64_t>(S) * (F / kUpOut);
-    hipLaunchKernelGGL(moe_up_i8_kernel, dim3(blocks_for(items, 256)), dim3(kUpThreads),
-                       static_cast<size_t>(rows) * (H + kPad) + slots_bytes(S, E), stream, static_cast<const uint16_t*>(x),
-                       topk_idx, S, k, E, H, F, up, up_scales, rows, h, most);
-    const hipError_t e = hipGetLastError();
+    const Call c = {x, topk_idx, topk_weights, T, k, E, H, F, up, up_scales, down, down_scales,
+                    h, reinterpret_cast<uint32_t*>(h + static_cast<int64_t>(T) * k * F), out, stream};
+    const hipError_t e = H < kTogether ? launch_up<true>(c) : launch_up<false>(c);
     if (e != hipSuccess) return e;
-    if (H <= 4096)
-        return launch_down<16>(h, most, topk_idx, topk_weights, T, k, E, H, F, down, down_scales, out, stream);
-    return launch_down<32>(h, most, topk_idx, topk_weights, T, k, E, H, F, down, down_scales, out, stream);
+    return H <= 4096 ? launch_down<16>(c) : launch_down<32>(c);
 }
 
 }  // namespace ep

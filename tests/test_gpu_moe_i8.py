@@ -45,7 +45,8 @@ class Layer:
         assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], ref[bad][:5], tol[bad][:5])
 
 
-@pytest.mark.parametrize("H,F,E", [(128, 128, 1), (128, 384, 8), (640, 128, 60), (1024, 512, 16), (4224, 256, 8), (256, 2176, 4)])
+@pytest.mark.parametrize("H,F,E", [(128, 128, 1), (128, 384, 8), (640, 128, 60), (1024, 512, 16), (4224, 256, 8), (256, 2176, 4),
+                                   (1920, 128, 20), (2048, 256, 8), (2176, 128, 60)])
 @pytest.mark.parametrize("T,k", [(1, 1), (1, 8), (3, 2), (16, 6), (64, 8)])
 def test_layer(T, k, H, F, E):
     layer = Layer(H, F, E)
