@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
 // by weight tiles: a wave keeps its token tiles of all 128 inputs in registers, and in
 // quarter q multiplies them with its weight tile q, while tile q + 1 is read and, in
 // the last quarter, the next stage's token tiles.  So a slot's parts are free again
-// one after the other, long before the stage ends, and are asked for anew 1.25 to 1.75
+// one after the other, long before the stage ends, and are asked for anew 1.25 to 1.5
 // stages before they are read.
 //
 // A row has eight places of 16 bytes in a slot; inputs 16 c .. + 15 of row r are at place
@@ -324,8 +324,8 @@ __device__ __forceinline__ void tile_item(const Call& c, const Item& it, const F
         b[u][i] = *reinterpret_cast<const i32x4*>(ring + (first ^ (u * 32)) + from + kTokenPart + (wx * kT + i) * 32 * kStage);
     };
     // Quarter q of the stage in the slot at `from` (the next one's at `next`): its
-    // products, between them reads, and its loads into this slot.  (In this
-    // order: left to itself the compiler reads an operand just before its first product.)
+    // products, between them reads, and its loads into this slot or (quarter 0) the
+    // next.  (In this order: left to itself the compiler reads an operand just before its first product.)
     auto quarter = [&](int q, uint32_t from, uint32_t next) {
         const int ask0 = i8_quarter(q).from, ask1 = i8_quarter(q).to;
 #pragma unroll
@@ -342,7 +342,8 @@ __device__ __forceinline__ void tile_item(const Call& c, const Item& it, const F
             // One every second product, or where there are few in turn.
 #pragma unroll
             for (int g = ask0; g < ask1; ++g)
-                if ((kT > 2 ? (g - ask0) * 2 : (g - ask0) % (4 * kT)) == m) ask<kSilu>(f, g, at_ring + from, wave);
+                if ((kT > 2 ? (g - ask0) * 2 : (g - ask0) % (4 * kT)) == m)
+                    ask<kSilu>(f, g, at_ring + (q == 0 ? next : from), wave);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -356,24 +357,23 @@ __device__ __forceinline__ void tile_item(const Call& c, const Item& it, const F
     // asked for anew behind quarter 0 at the earliest.  kMore: the last item's stores, if
     // there were as many as this one makes, and this one's two loads of scales.
     constexpr int kStores = (kSilu ? 4 : 8) * kT, kMore = kStores + 2;
-    const int stages = c.K / kStage, early = stored == kStores ? 2 : 0;
-    static_assert(i8_quarter(0).early == 2 && i8_quarter(1).early == 2 && i8_quarter(2).early == 1 &&
-                      i8_quarter(3).early == 1, "as below");
-    for (int s = 0; s < stages; ++s) {
+    const int stages = c.K / kStage;
+    bool early = stored == kStores;
+    for (int s = 0; s < stages; ++s, early = false) {
         const uint32_t next = here ^ kSlot;
         quarter(0, here, next);
-        wait<i8_quarter(0).later, kMore>(s < early);
+        advance();
+        wait<i8_quarter(0).later, kMore>(early);
         meet();
         quarter(1, here, next);
-        wait<i8_quarter(1).later, kMore>(s < early);
+        wait<i8_quarter(1).later, kMore>(early);
         meet();
         quarter(2, here, next);
-        wait<i8_quarter(2).later, kMore>(s + 1 < early);
+        wait<i8_quarter(2).later, kMore>(early);
         meet();
         quarter(3, here, next);
-        wait<i8_quarter(3).later, kMore>(s + 1 < early);
+        wait<i8_quarter(3).later, kMore>(early);
         meet<false>();
-        advance();
         here = next;
     }
     stored = kStores;
@@ -456,13 +456,14 @@ __global__ __launch_bounds__(kThreads, 1) void tile_i8_kernel(Call c) {
             f.stage = stages - 1;
         }
     };
+    // Of the second stage all but what its first quarter asks for.
+    constexpr int kRest = i8_quarter(0).from;
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
+    for (int i = 0; i < kLoads; ++i) ask<kSilu>(f, i, at_ring, wave);
+    advance();
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) ask<kSilu>(f, i, at_ring + d * kSlot, wave);
-        advance();
-    }
-    arrive<kLoads>();
+    for (int i = 0; i < kRest; ++i) ask<kSilu>(f, i, at_ring + kSlot, wave);
+    arrive<kRest>();
     uint32_t here = 0;
     int odd = 0, stored = 0;                        // stores of the last item
     for (; walk.left > 0; walk.on(), odd ^= 1) {

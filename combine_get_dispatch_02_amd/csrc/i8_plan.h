@@ -33,27 +33,29 @@ constexpr bool i8_streams(int64_t num_rows, int E, int K, int N, bool silu) {
 
 // A wave's loads of a stage (128 inputs): 0 .. 7 bring token rows, 8 + 2 q and 9 + 2 q
 // rows of the weight tiles q.  While a stage is worked off, the loads of the stage after
-// next go to its slot, from those whose rows every wave has read.
+// next go to its slot, from those whose rows every wave has read, and the last four a
+// quarter into the next stage, for quarter 3 is busy with reads.
 constexpr int kLoads8 = 16;
 
-// Quarter q of a stage: loads `from` .. `to` - 1 are asked for in it.  Behind it the
-// waves wait for what the next quarter reads: behind quarters 0 and 1 weight tiles 2
-// and 3 of the same stage, behind 2 the next stage's token tiles and weight tiles 0,
-// behind 3 its weight tiles 1; that is until at most `later` accesses are on the way.
-// Loads arrive in the order in which they were asked for, and `later` counts those that
-// follow: behind quarter 0 tiles 3 (2) and the next stage (16); behind 1 the next stage
-// and quarter 1's (6); behind 2 tiles 1, 2 and 3 (6) and quarters 1 and 2 (12); behind 3
-// tiles 2 and 3 (4) and quarters 1, 2 and 3 (16).
+// Quarter q of a stage: loads `from` .. `to` - 1 are asked for in it, of the stage after
+// next, or (quarter 0) of the next.  Behind it the waves wait for what the next quarter
+// reads: behind quarters 0 and 1 weight tiles 2 and 3 of the same stage, behind 2 the next
+// stage's token tiles and weight tiles 0, behind 3 its weight tiles 1; that is until at
+// most `later` accesses are on the way.  Loads arrive in the order in which they were
+// asked for, and `later` counts those that follow: behind quarter 0 tiles 3 (2), the last
+// stage's quarters 1 and 2 (12) and this one's quarter 0 (4); behind 1 the same 12, and
+// quarters 0 and 1 (10); behind 2 tiles 1 (2) and quarters 0, 1 and 2 (16); behind 3
+// these 16.
 //
 // Between two items' stages a wave stores the first one's results and asks for the
-// scales of the second.  Behind quarters of the first `early` stages of an item these
-// too follow what is waited for, and may be counted.
+// scales of the second.  In an item's first stage these too follow what is waited for,
+// and may be counted.
 struct I8Quarter {
-    int from, to, later, early;
+    int from, to, later;
 };
 constexpr I8Quarter i8_quarter(int q) {
-    return q == 0 ? I8Quarter{0, 0, 18, 2} : q == 1 ? I8Quarter{0, 6, 22, 2} : q == 2 ? I8Quarter{6, 12, 18, 1}
-                                                                                : I8Quarter{12, 16, 20, 1};
+    return q == 0 ? I8Quarter{12, 16, 18} : q == 1 ? I8Quarter{0, 6, 22} : q == 2 ? I8Quarter{6, 12, 18}
+                                                                                  : I8Quarter{0, 0, 16};
 }
 
 }  // namespace ep

@@ -13,7 +13,7 @@ SOURCE = r"""
 #include "i8_plan.h"
 extern "C" void quarter(int q, int* out) {
     const ep::I8Quarter s = ep::i8_quarter(q);
-    out[0] = s.from; out[1] = s.to; out[2] = s.later; out[3] = s.early;
+    out[0] = s.from; out[1] = s.to; out[2] = s.later;
 }
 extern "C" int streams(long long num_rows, int E, int K, int N, int silu) {
     return ep::i8_streams(num_rows, E, K, N, silu != 0);
@@ -32,8 +32,8 @@ def lib():
 
 
 def quarter(q):
-    """(from, to, later, early)"""
-    out = (ctypes.c_int * 4)()
+    """(from, to, later)"""
+    out = (ctypes.c_int * 3)()
     lib().quarter(q, out)
     return tuple(out)
 
