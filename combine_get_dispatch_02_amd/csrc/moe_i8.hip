@@ -7,11 +7,14 @@
 //   down  casts h, multiplies it with the experts' down rows, and adds each token's
 //         slots with their weights.
 //
-// Bound by reading the weights of the experts that some slot chose, once each.  The
-// slots are grouped by expert in every block anew (at most kMaxSlots ids), so that
-// no launch has to do it before; the casts too are done by every block for what it needs,
-// out of the caches.  Sums of products are integers, so no order changes a result;
-// each token's slots are added in slot order.
+// Bound by reading the weights of the experts that some slot chose, once each: 16 tokens,
+// 8 of 256 experts, 7168 -> 2048 (4.5 GB) 760-790 us, 5.8 TB/s; one token (353 MB) 79 us,
+// 4.5 TB/s (up 48, down 31), of which a launch's start (the slots, the casts, the first
+// loads) is 6 us or more.  What is left at 64 tokens, 6 of 64 experts, 4096 -> 1024 (805 MB,
+// 187 us, 4.3 TB/s) are the casts of h, 384 rows in every block of down.  The slots are grouped by expert in every block anew (at most kMaxSlots ids), so
+// that no launch has to do it before; the casts too are done by every block for what it
+// needs, out of the caches.  Sums of products are integers, so no order changes a
+// result; each token's slots are added in slot order.
 #include "moe_launch.h"
 #include "quant_i8.h"
 #include "stream_i8.h"
@@ -164,8 +167,10 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // An item is 32 gate rows and their 32 up rows of an expert against a tile of its slots.
 // A block's eight waves take a run of items together, splitting each item's inputs and
 // joining their sums in shared memory; or (kAlone), where there are few inputs to split,
-// each wave takes a run of its own, and no wave waits for another.  Loads run on from one item to the next.  The tokens of a tile are cast into
-// shared memory when its first item comes.
+// each wave takes a run of its own, and no wave waits for another.  Loads run on from one
+// item to the next; with two steps on the way both launches take 80 us for one token, with
+// three 83 and with four 88 (16 tokens: 787, 791, 794).  The tokens of a tile are cast
+// into shared memory when its first item comes.
 constexpr int kUpThreads = 512, kUpWaves = kUpThreads / kWave, kUpDeep = 2;
 constexpr int kUpShared = 126 * 1024;               // bytes of a CU's 160 KB beside what is declared below
 constexpr int kUpOut = 32;                          // outputs of an item
@@ -380,9 +385,9 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
 // shared memory for them.  Eight waves multiply: a chunk's products, tile
 // after tile and 128 inputs at a time, are one row of steps of which each takes an
 // eighth; their loads run on from one chunk to the next, and sums meet in shared memory
-// by integer additions.  Eight more waves cast the next chunk's h meanwhile.  (The same
-// by all waves between the chunks had loads on the way for a third of the time only:
-// 64 tokens over 64 experts, 1024 -> 4096, 126 us.)
+// by integer additions.  Eight more waves cast the next chunk's h meanwhile.  (Both
+// launches for 64 tokens, 6 of 64 experts, 4096 -> 1024: by the same eight waves, between the
+// chunks, 270 us; four of them beside eight 199; eight 187, of which down takes 88.)
 constexpr int kDownWaves = 8, kCastWaves = 8, kDownThreads = (kDownWaves + kCastWaves) * kWave;
 constexpr int kDownCodes = 32 * 1024;               // a chunk's codes at most
 constexpr int kDownRoom = 34 * 1024;                // and the bytes they take with their padding
@@ -469,11 +474,13 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
         auto begin = [&](Piece& x, int p) {
             x = {p, 0, p < c.p1 - c.p0 ? uniform(s.order[c.p0 + p]) : S};
         };
-        // (Past a row's end the next row's are read, past the chunk's last row nothing.)
+        // (Past a row's end the next row's are read, past the chunk's last row nothing: there
+        // the lanes' own offsets, which alone are held against its size for sure, are
+        // behind the buffer's end.)
         auto ask = [&](int b) {
 #pragma unroll
             for (int e = 0; e < kKeep; ++e) {
-                v[b][e] = __builtin_bit_cast(f32x4, load16(from, lane * 16, asked.row * F * 4 + asked.i * kWave * 16));
+                v[b][e] = __builtin_bit_cast(f32x4, load16(from, asked.row * F * 4 + (asked.i * kWave + lane) * 16, 0));
                 if (++asked.i == pieces) begin(asked, asked.p + kCastWaves);
             }
         };
