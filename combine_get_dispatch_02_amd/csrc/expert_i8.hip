@@ -26,29 +26,6 @@ struct Call {
     uint16_t* y;
 };
 
-// What an item's waves read: weight rows from n0 on (w[1]: the up rows that belong to
-// them), their scales, and token rows from row0 on.
-struct Operands {
-    int64_t row0;
-    int n0, left;                                   // first output, token rows left
-    Buffer w[2], x;
-    const float* w_scales[2];
-};
-template <bool kSilu>
-__device__ __forceinline__ Operands operands(const Call& c, int e, int64_t row0, int left, int n0, int wide, int deep) {
-    const int64_t w0 = static_cast<int64_t>(e) * (kSilu ? 2 * c.N : c.N) + n0, up = kSilu ? c.N : 0;
-    const int64_t rows = c.N - n0 < wide ? c.N - n0 : wide, tokens = left < deep ? left : deep;
-    return {row0, n0, left,
-            {buffer(c.w + w0 * c.K, rows * c.K), buffer(c.w + (w0 + up) * c.K, rows * c.K)},
-            buffer(c.x + row0 * c.K, tokens * c.K),
-            {c.w_scales + w0, c.w_scales + w0 + up}};
-}
-// Weight row n of an item's; those past the outputs repeat the last one, and what they
-// give is not stored.
-__device__ __forceinline__ uint32_t weight_row(const Operands& o, int n, int N) {
-    return o.n0 + n < N ? n : N - 1 - o.n0;
-}
-
 // Four outputs, in fp32.
 __device__ __forceinline__ f32x4 scaled(const i32x4& sum, float x_scale, const f32x4& w_scale) {
     f32x4 v;
@@ -66,11 +43,38 @@ __device__ __forceinline__ f32x4 scales4(const float* scales, int n) {
     return *reinterpret_cast<const f32x4*>(scales + n);
 }
 
-// ---- few rows per expert: bound by reading the weights ---------------------------
+// ---- few items: bound by reading the weights -------------------------------------------
 // A wave takes 64 weight rows (kSilu: 32 gate rows and their 32 up rows) and up to 16
 // token rows.  Where there are items for every wave, each takes whole items; where
 // there are not, the four waves of a block split an item's inputs, so that every CU has
-// loads in flight, and join their sums in shared memory.
+// loads in flight, and join their sums in shared memory.  One token's 8 of 256 experts,
+// 7168 -> 2 x 2048 (235 MB): 46 us, 5.2 TB/s.  (One step on the way 45, three 49, four 53: past
+// its end a wave asks for its last step again.  8 experts of 16 rows, 4096 -> 4096: 34
+// with any; by tiles 61.)  Which calls these are: i8_streams().
+//
+// What an item's waves read: weight rows from n0 on (w[1]: the up rows that belong to
+// them), their scales, and token rows from row0 on.
+struct Operands {
+    int n0;
+    Buffer w[2], x;
+    const float* w_scales[2];
+};
+template <bool kSilu>
+__device__ __forceinline__ Operands operands(const Call& c, int e, int64_t row0, int left, int n0) {
+    constexpr int kWide = kSilu ? 32 : 64;
+    const int64_t w0 = static_cast<int64_t>(e) * (kSilu ? 2 * c.N : c.N) + n0, up = kSilu ? c.N : 0;
+    const int64_t rows = c.N - n0 < kWide ? c.N - n0 : kWide, tokens = left < 16 ? left : 16;
+    return {n0,
+            {buffer(c.w + w0 * c.K, rows * c.K), buffer(c.w + (w0 + up) * c.K, rows * c.K)},
+            buffer(c.x + row0 * c.K, tokens * c.K),
+            {c.w_scales + w0, c.w_scales + w0 + up}};
+}
+// Weight row n of an item's; those past the outputs repeat the last one, and what they
+// give is not stored.
+__device__ __forceinline__ uint32_t weight_row(const Operands& o, int n, int N) {
+    return o.n0 + n < N ? n : N - 1 - o.n0;
+}
+
 template <bool kSilu>
 __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
     constexpr int kOut = kSilu ? 32 : 64;           // outputs of an item
@@ -95,7 +99,7 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
         const int m0 = (tile - t.start[e]) * 16;
         const int left = __builtin_amdgcn_readfirstlane(t.count[e] - m0);
         const int64_t row0 = __builtin_amdgcn_readfirstlane(t.first[e]) + static_cast<int64_t>(m0);
-        const Operands o = operands<kSilu>(c, e, row0, left, column * kOut, kOut, 16);
+        const Operands o = operands<kSilu>(c, e, row0, left, column * kOut);
         uint32_t row[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -104,7 +108,7 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
         auto weights = [&](int j) { return o.w[kSilu ? j / 2 : 0]; };
         auto tokens = [&](int h, int at) { return load16(o.x, mine_x, at + 64 * h); };
         i32x4 acc[4] = {};
-        Stream8<4, kDeep, true> s;
+        Stream8<4, kDeep> s;
         const int k = split ? wave * 128 : 0, step = split ? 512 : 128;
         s.start(k, step, c.K, row, weights, tokens);
         s.run(k, step, c.K, row, weights, tokens, acc);
@@ -139,7 +143,7 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
     }
 }
 
-// ---- many rows per expert: bound by the matrix unit, or by reading the weights --------
+// ---- tiles: bound by reading the weights, or with many rows by the matrix unit -----------
 // One item: up to 256 token rows x 256 weight rows (kSilu: 128 gate rows and their 128
 // up rows).  Four waves, one a SIMD, two by two: each has 128 weight rows (kSilu: 64 of
 // either) and half of the token rows, in tiles of 32 x 32 (v_mfma_i32_32x32x32_i8).  Both
@@ -159,6 +163,14 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
 // c ^ (r / 2 % 8), so that any 16 neighbouring rows' places c lie in different banks.
 // A lane holds row l % 32 of either operand, and inputs 32 u + 16 (l / 32) .. + 15 in step
 // u of a stage's four.
+//
+// 256 experts with 128 rows on average, 7168 -> 2 x 2048 (7.9 GB): 1.44-1.50 ms, 5.3-5.5
+// TB/s.  64 with 768, 4096 -> 2 x 1024: 410-450 us, 1.8-2.0 POP/s; half of its cycles are
+// the matrix unit's, at the 1.5-1.7 GHz that the card's power leaves (a loop of products
+// alone runs at 3.0-3.2 POP/s), and what nothing hides are the results (an exponential
+// and a reciprocal each: 10 of some 100 thousand cycles an item).  Stages of 64 inputs in
+// a ring of four: 506 us for it; 128-byte rows: 461; parts asked for by quarters: 429;
+// with the last quarter's loads in the next stage's first, beside fewer reads: 411.
 
 // 16 (or 4) bytes a lane past the registers to shared memory at byte `to` + 16 lane
 // (+ 4 lane).  By hand: the compiler takes any later read of shared memory for one of
@@ -303,7 +315,8 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
 }
 
 // One item of up to 64 kT token rows: its stages, of which the first lies in the slot at
-// `here`, and its results.  stored: the stores of the item before.  advance() moves the loading side on by a stage.
+// `here`, and its results.  stored: the stores of the item before.  advance() moves the
+// loading side on by a stage.
 template <bool kSilu, int kT, typename Advance>
 __device__ __forceinline__ void tile_item(const Call& c, const Item& it, const Fill& f, Advance advance,
                                           const uint8_t* ring, uint32_t at_ring, const float* scales, uint32_t& here,
@@ -325,7 +338,8 @@ __device__ __forceinline__ void tile_item(const Call& c, const Item& it, const F
     };
     // Quarter q of the stage in the slot at `from` (the next one's at `next`): its
     // products, between them reads, and its loads into this slot or (quarter 0) the
-    // next.  (In this order: left to itself the compiler reads an operand just before its first product.)
+    // next.  (In this order: left to itself the compiler reads an operand just before
+    // its first product.)
     auto quarter = [&](int q, uint32_t from, uint32_t next) {
         const int ask0 = i8_quarter(q).from, ask1 = i8_quarter(q).to;
 #pragma unroll

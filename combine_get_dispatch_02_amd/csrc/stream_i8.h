@@ -18,12 +18,11 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // weights(j) is the buffer of weight tile j, and row[j] the lane's offset in it: that of
 // its weight row, and 16 q.  tokens(h, at) gives the lane's 16 codes of its token row
 // at inputs at + 64 h + 16 q.  K is a multiple of 128, so a step takes whole 128-byte
-// lines of each row; kDeep steps are on the way at a time.  kAhead: the token rows come
-// from memory, and are asked for before the weights that they meet (loads return in
-// order); else from shared memory, when they are needed.
-template <int kTiles, int kDeep, bool kAhead>
+// lines of each row; kDeep steps are on the way at a time.  The token rows
+// are asked for before the weights that they meet, for loads return in order.
+template <int kTiles, int kDeep>
 struct Stream8 {
-    u32x4 w[kDeep][kTiles][2], v[kAhead ? kDeep : 1][2];
+    u32x4 w[kDeep][kTiles][2], v[kDeep][2];
 
     // Every load is made on every way through the loop, past the end the last step's
     // again: a branch around a load makes the compiler wait for all that are on the way.
@@ -32,10 +31,8 @@ struct Stream8 {
                                          Tokens tokens) {
         at = at < K ? at : K - 128;
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (kAhead) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) v[buf][h] = tokens(h, at);
-        }
+        for (int h = 0; h < 2; ++h) v[buf][h] = tokens(h, at);
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
 #pragma unroll
@@ -57,13 +54,11 @@ struct Stream8 {
                 const int at = k + b * step;
                 if (at < K) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const u32x4 t = kAhead ? v[kAhead ? b : 0][h] : tokens(h, at);
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int j = 0; j < kTiles; ++j)
                             acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[b][j][h]),
-                                                                           __builtin_bit_cast(i32x4, t), acc[j], 0, 0, 0);
-                    }
+                                                                           __builtin_bit_cast(i32x4, v[b][h]), acc[j], 0, 0, 0);
                 }
                 load(b, at + kDeep * step, K, row, weights, tokens);
             }

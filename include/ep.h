@@ -11,8 +11,8 @@
  *     128 channels (low-latency port commit, dispatch<kUseFP8,...>),
  *   - combine consuming the receiver-side layout produced by dispatch (commit
  *     fixing internode HT combine: receiver-side prefix sums),
- * and, around that path, routing, the experts' products with 4-bit weights and
- * the gradients of routing and combine.
+ * and, around that path, routing, the experts' products with 4-bit weights, the
+ * experts' layer in 8-bit integers and the gradients of routing and combine.
  * On one GPU every destination "rank" is a contiguous range of one receive
  * buffer in this GPU's HBM: experts are split into num_ranks contiguous
  * blocks of num_experts/num_ranks, and rank r's rows are
@@ -494,7 +494,8 @@ int ep_expert_linear_w4(const void* x, int64_t num_rows, const int32_t* expert_r
  *                (num_experts and capacity are then ignored).
  *   x_i8         [num_rows, hidden] int8  out (16-byte aligned)
  *   x_scales     [num_rows]         fp32  out
- * Requires hidden % 16 == 0, 0 <= num_rows < 2^31.  No workspace.
+ * Requires hidden % 16 == 0, 0 <= num_rows < 2^31.  The outputs must not overlap x.
+ * No workspace.
  * ------------------------------------------------------------------------- */
 int ep_dispatch_i8(const void* x, const int64_t* topk_idx, const float* topk_weights,
                    int64_t num_tokens, int hidden, int num_topk, int num_experts, int num_ranks,
@@ -534,7 +535,8 @@ int ep_quantize_i8(const void* x, int64_t num_rows, int hidden, const int32_t* e
  *   y           [num_rows, out_features]  bf16  out (16-byte aligned)
  * Requires in_features % 128 == 0, out_features % 8 == 0, both positive,
  * in_features <= EP_MAX_IN_FEATURES_I8, out_features <= EP_MAX_OUT_FEATURES_I8,
- * 1 <= E <= EP_MAX_EXPERTS, 0 <= num_rows < 2^31, capacity >= 0.  y must not overlap the inputs.  No workspace.
+ * 1 <= E <= EP_MAX_EXPERTS, 0 <= num_rows < 2^31, capacity >= 0.  y must not overlap
+ * the inputs.  No workspace.
  * ------------------------------------------------------------------------- */
 #define EP_MAX_IN_FEATURES_I8 (1 << 16)
 #define EP_MAX_OUT_FEATURES_I8 (1 << 22)
@@ -564,9 +566,10 @@ int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_r
  *   down_i8       [E, H, F]   int8  in, down_scales [E, H] fp32 in (all 16-byte aligned)
  *   out           [T, H]      bf16  out (16-byte aligned)
  * Requires T*k <= EP_MOE_MAX_SLOTS, H % 128 == 0, F % 128 == 0, both positive,
- * H <= EP_MAX_IN_FEATURES_I8, F <= EP_MOE_MAX_FFN, 1 <= E <= EP_MAX_EXPERTS, 1 <= k <= EP_MAX_TOPK.  out must
- * not overlap the inputs.  Workspace: ep_moe_i8_workspace_bytes(T, k, F), 16-byte
- * aligned; calls that may run at the same time need one each.
+ * H <= EP_MAX_IN_FEATURES_I8, F <= EP_MOE_MAX_FFN, 1 <= E <= EP_MAX_EXPERTS,
+ * 1 <= k <= EP_MAX_TOPK.  out must not overlap the inputs.  Workspace:
+ * ep_moe_i8_workspace_bytes(T, k, F), 16-byte aligned; calls that may run at the same
+ * time need one each.
  * ------------------------------------------------------------------------- */
 #define EP_MOE_MAX_SLOTS 512
 #define EP_MOE_MAX_FFN (1 << 15)
