@@ -11,7 +11,7 @@
 // 8 of 256 experts, 7168 -> 2048 (4.5 GB) 760-790 us, 5.8 TB/s; one token (353 MB) 79 us,
 // 4.5 TB/s (up 48, down 31), of which a launch's start (the slots, the casts, the first
 // loads) is 6 us or more.  What is left at 64 tokens, 6 of 64 experts, 4096 -> 1024 (805 MB,
-// 187 us, 4.3 TB/s) are the casts of h, 384 rows in every block of down.  The slots are grouped by expert in every block anew (at most kMaxSlots ids), so
+// 186 us, 4.3 TB/s) are the casts of h, 384 rows in every block of down.  The slots are grouped by expert in every block anew (at most kMaxSlots ids), so
 // that no launch has to do it before; the casts too are done by every block for what it
 // needs, out of the caches.  Sums of products are integers, so no order changes a
 // result; each token's slots are added in slot order.
@@ -387,7 +387,8 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
 // eighth; their loads run on from one chunk to the next, and sums meet in shared memory
 // by integer additions.  Eight more waves cast the next chunk's h meanwhile.  (Both
 // launches for 64 tokens, 6 of 64 experts, 4096 -> 1024: by the same eight waves, between the
-// chunks, 270 us; four of them beside eight 199; eight 187, of which down takes 88.)
+// chunks, 270 us; four of them beside eight 199; eight 186.  Of down's 86 us, 30 go if h is
+// not read, and 8 if the weights come out of the L2: h and weights share the CU's way in.)
 constexpr int kDownWaves = 8, kCastWaves = 8, kDownThreads = (kDownWaves + kCastWaves) * kWave;
 constexpr int kDownCodes = 32 * 1024;               // a chunk's codes at most
 constexpr int kDownRoom = 34 * 1024;                // and the bytes they take with their padding
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
     // Every wave meets the others once before the first chunk's cast, once behind it, and
     // once behind each chunk but the last.
     if (wave >= kDownWaves) {
-        constexpr int kThreads = kCastWaves * kWave, kKeep = 8;
+        constexpr int kThreads = kCastWaves * kWave, kKeep = 4;
         const int mine = me - kDownWaves * kWave, vectors = F / 4, pieces = (vectors + kWave - 1) / kWave;
         for (int p = mine; p < places; p += kThreads) {
             const int columns = F / kUpOut / 4;     // in vectors of four
@@ -463,66 +464,72 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
         }
         __syncthreads();
         // Pieces of 64 vectors of four of a place's h, place by place, every kCastWaves-th
-        // of them this wave's.  The next kKeep are asked for before these are cast.
+        // of them this wave's.  The next kKeep, of the same chunk or the next one, are asked
+        // for before these are cast; in every chunk a wave has at least one such batch,
+        // however few pieces there are for it.
         struct Piece {
             int p, i, row;
         };
         f32x4 v[2][kKeep];
-        Chunk c = chunk_from(s, 0, chunk_slots);
+        Chunk c = chunk_from(s, 0, chunk_slots), a = c;                         // cast, asked for
         const Buffer from = buffer(h, static_cast<int64_t>(S) * F * 4);
         Piece asked = {};
-        auto begin = [&](Piece& x, int p) {
-            x = {p, 0, p < c.p1 - c.p0 ? uniform(s.order[c.p0 + p]) : S};
+        bool all = false;                           // of chunk a are asked for
+        auto begin = [&](int p) {
+            asked = {p, 0, p < a.p1 - a.p0 ? uniform(s.order[a.p0 + p]) : S};
         };
         // (Past a row's end the next row's are read, past the chunk's last row nothing: there
         // the lanes' own offsets, which alone are held against its size for sure, are
         // behind the buffer's end.)
         auto ask = [&](int b) {
+            if (all) {
+                a = chunk_from(s, a.t1, chunk_slots);
+                begin(wave - kDownWaves);
+            }
 #pragma unroll
             for (int e = 0; e < kKeep; ++e) {
                 v[b][e] = __builtin_bit_cast(f32x4, load16(from, asked.row * F * 4 + (asked.i * kWave + lane) * 16, 0));
-                if (++asked.i == pieces) begin(asked, asked.p + kCastWaves);
+                if (++asked.i == pieces) begin(asked.p + kCastWaves);
+            }
+            all = asked.p >= a.p1 - a.p0;
+        };
+        Piece at = {wave - kDownWaves, 0, 0};
+        int odd = 0;
+        auto cast = [&](int b) {
+#pragma unroll
+            for (int e = 0; e < kKeep; ++e) {
+                if (at.p >= c.p1 - c.p0) break;
+                const float by = casts[c.p0 + at.p][1];
+                // 127 h / a by the product with 127 / a: the quotient's own error is that of fp32.
+                uint32_t code[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) code[x] = __float_as_uint(__builtin_fmaf(v[b][e][x], by, 12582912.0f));
+                const uint32_t lo = __builtin_amdgcn_perm(code[1], code[0], 0x0C0C0400u);
+                const uint32_t hi = __builtin_amdgcn_perm(code[3], code[2], 0x04000C0Cu);
+                const int vec = at.i * kWave + lane;
+                if (vec < vectors)
+                    *reinterpret_cast<uint32_t*>(codes + odd * half + at.p * stride + vec * 4) = by == 0.0f ? 0u : lo | hi;
+                if (++at.i == pieces) {
+                    at.i = 0;
+                    at.p += kCastWaves;
+                }
             }
         };
-        begin(asked, wave - kDownWaves);
+        begin(wave - kDownWaves);
         if (places > 0) ask(0);
-        for (int odd = 0; c.t0 < s.tiles; odd ^= 1) {
-            const int n = c.p1 - c.p0, p0 = c.p0;
-            Piece at = {wave - kDownWaves, 0, 0};
-            auto cast = [&](int b) {
+        while (c.t0 < s.tiles)
 #pragma unroll
-                for (int e = 0; e < kKeep; ++e) {
-                    if (at.p >= n) break;
-                    const float by = casts[p0 + at.p][1];
-                    // 127 h / a by the product with 127 / a: the quotient's own error is that of fp32.
-                    uint32_t code[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) code[x] = __float_as_uint(__builtin_fmaf(v[b][e][x], by, 12582912.0f));
-                    const uint32_t lo = __builtin_amdgcn_perm(code[1], code[0], 0x0C0C0400u);
-                    const uint32_t hi = __builtin_amdgcn_perm(code[3], code[2], 0x04000C0Cu);
-                    const int vec = at.i * kWave + lane;
-                    if (vec < vectors)
-                        *reinterpret_cast<uint32_t*>(codes + odd * half + at.p * stride + vec * 4) = by == 0.0f ? 0u : lo | hi;
-                    if (++at.i == pieces) {
-                        at.i = 0;
-                        at.p += kCastWaves;
-                    }
+            for (int b = 0; b < 2; ++b) {
+                if (c.t0 >= s.tiles) break;
+                ask(1 - b);
+                cast(b);
+                if (at.p >= c.p1 - c.p0) {          // the chunk is cast, and a the next one
+                    __syncthreads();
+                    c = a;
+                    at = {wave - kDownWaves, 0, 0};
+                    odd ^= 1;
                 }
-            };
-            // Behind the chunk's last pieces the next chunk's first are asked for, before
-            // the waves meet.
-            do {
-                ask(1);
-                cast(0);
-                if (at.p >= n) break;
-                ask(0);
-                cast(1);
-            } while (at.p < n);
-            c = chunk_from(s, c.t1, chunk_slots);
-            begin(asked, wave - kDownWaves);
-            if (c.t0 < s.tiles) ask(0);
-            __syncthreads();
-        }
+            }
     } else {
         const int steps = F / 128;
         for (int i = me; i < S * kRows; i += kDownWaves * kWave) sums[i] = 0;
@@ -716,7 +723,8 @@ hipError_t launch_down(const Call& c) {
     // Parts of the tokens where a quarter of the CUs or more would have no block.  (Both
     // launches, one part against as many as this: 30 tokens, 6 of 128 experts, 384 -> 1408,
     // 147 / 77 us; 64, 4 of 64, 1024 -> 768, 82 / 63; 64, 8 of 256, 2048 -> 768, 260 / 231.)
-    const int blocks = c.H / kRows, most_parts = blocks >= 192 ? 1 : 256 / blocks, parts = most_parts < c.T ? most_parts : c.T;
+    const int blocks = c.H / kRows;
+    const int most_parts = blocks >= 192 ? 1 : 256 / blocks, parts = most_parts < c.T ? most_parts : c.T;
     const int S = (c.T + parts - 1) / parts * c.k, stride = c.F + kPad;
     static_assert(kMoeMaxFfn <= kDownCodes, "a slot's codes fit");
     int chunk = kDownCodes / c.F < kDownRoom / stride ? kDownCodes / c.F : kDownRoom / stride;
@@ -742,7 +750,14 @@ hipError_t launch_moe_i8(const void* x, const int64_t* topk_idx, const float* to
                     h, reinterpret_cast<uint32_t*>(h + static_cast<int64_t>(T) * k * F), out, stream};
     const hipError_t e = H < kTogether ? launch_up<true>(c) : launch_up<false>(c);
     if (e != hipSuccess) return e;
-    return H <= 4096 ? launch_down<16>(c) : launch_down<32>(c);
+    // Outputs of a block of down.  16 where H leaves many a block; but many slots an expert
+    // are better split over twice the parts, for then the casts of h are what a block
+    // reads most (us, 16 against 32 outputs: 64 tokens, 8 of 16 experts, 4096 -> 1408, 204 / 164;
+    // 8 of 32, 4096 -> 1024, 174 / 151; 8 of 8, 2048 -> 1408, 102 / 81; 16, 8 of 8, 4096 -> 2048,
+    // 87 / 82; 64, 4 of 16, 2048 -> 2048, 105 / 106; but 8 of 64, 2048 -> 1408, 171 / 180; 6 of
+    // 64, 4096 -> 1024, 188 / 192; 1, 8 of 64, 2048 -> 768, 27 / 29).
+    const bool wide = H > 4096 || T * k >= 16 * E;
+    return wide ? launch_down<32>(c) : launch_down<16>(c);
 }
 
 }  // namespace ep
