@@ -387,7 +387,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
 // eighth; their loads run on from one chunk to the next, and sums meet in shared memory
 // by integer additions.  Eight more waves cast the next chunk's h meanwhile.  (Both
 // launches for 64 tokens, 6 of 64 experts, 4096 -> 1024: by the same eight waves, between the
-// chunks, 270 us; four of them beside eight 199; eight 186.  Of down's 86 us, 30 go if h is
+// chunks, 270 us; four of them beside eight 199; eight 186.  Of 88 us of down, 30 go if h is
 // not read, and 8 if the weights come out of the L2: h and weights share the CU's way in.)
 constexpr int kDownWaves = 8, kCastWaves = 8, kDownThreads = (kDownWaves + kCastWaves) * kWave;
 constexpr int kDownCodes = 32 * 1024;               // a chunk's codes at most
