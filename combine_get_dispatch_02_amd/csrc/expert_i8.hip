@@ -175,6 +175,7 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
 // 16 (or 4) bytes a lane past the registers to shared memory at byte `to` + 16 lane
 // (+ 4 lane).  By hand: the compiler takes any later read of shared memory for one of
 // what such a load writes, and waits for it.  Whoever reads the bytes waits by arrive().
+// (m0 is set here alone: nothing else in these kernels uses it.)
 typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void load_past(uint32_t to, const Words4& from, uint32_t lane_offset, uint32_t offset) {
 #ifdef __HIP_DEVICE_COMPILE__
