@@ -8,8 +8,8 @@
 //         slots with their weights.
 //
 // Bound by reading the weights of the experts that some slot chose, once each: 16 tokens,
-// 8 of 256 experts, 7168 -> 2048 (4.5 GB) 760-790 us, 5.8 TB/s; one token (353 MB) 79 us,
-// 4.5 TB/s (up 48, down 31), of which a launch's start (the slots, the casts, the first
+// 8 of 256 experts, 7168 -> 2048 (4.5 GB) 760-790 us, 5.8 TB/s; one token (353 MB) 78 us,
+// 4.5 TB/s (up 48, down 30), of which a launch's start (the slots, the casts, the first
 // loads) is 6 us or more.  What is left at 64 tokens, 6 of 64 experts, 4096 -> 1024 (805 MB,
 // 186 us, 4.3 TB/s) are the casts of h, 384 rows in every block of down.  The slots are grouped by expert in every block anew (at most kMaxSlots ids), so
 // that no launch has to do it before; the casts too are done by every block for what it
@@ -647,10 +647,15 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
                 load(d);
             }
     }
-    // Places of the slots.
-    int32_t* place = reinterpret_cast<int32_t*>(codes);
+    // Places of the slots, and experts of the places (read out of topk_idx again, the scales
+    // would be asked for two loads' time later: one token 80 against 78 us).
+    int32_t *place = reinterpret_cast<int32_t*>(codes), *expert = place + S;
     __syncthreads();                                // behind the last chunk
     for (int i = me; i < S; i += kDownThreads) place[i] = -1;
+    for (int i = me; i < s.tiles * 16; i += kDownThreads) {
+        const int at = s.first[i / 16] + i % 16;
+        if (at < s.first[i / 16 + 1]) expert[at] = s.expert[i / 16];
+    }
     __syncthreads();
     for (int i = me; i < places; i += kDownThreads) place[s.order[i]] = i;
     __syncthreads();
@@ -668,7 +673,7 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
             for (int j = 0; j < kBatch; ++j) {
                 const int slot = t * k + (j0 + j < k ? j0 + j : k - 1);
                 p[j] = j0 + j < k ? place[slot] : -1;
-                const int64_t e = p[j] >= 0 ? topk_idx[slot] : 0;
+                const int64_t e = p[j] >= 0 ? expert[p[j]] : 0;
                 ws[j] = *reinterpret_cast<const f32x2*>(down_scales + e * H + n0 + n);
                 weight[j] = topk_weights ? topk_weights[slot] : 1.0f;
             }
