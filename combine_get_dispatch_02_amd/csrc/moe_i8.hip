@@ -168,10 +168,10 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // A block's eight waves take a run of items together, splitting each item's inputs and
 // joining their sums in shared memory; or (kAlone), where there are few inputs to split,
 // each wave takes a run of its own, and no wave waits for another.  Loads run on from one
-// item to the next; with two steps on the way both launches take 80 us for one token, with
-// three 83 and with four 88 (16 tokens: 787, 791, 794).  The tokens of a tile are cast
-// into shared memory when its first item comes.
-constexpr int kUpThreads = 512, kUpWaves = kUpThreads / kWave, kUpDeep = 2;
+// item to the next, one step of a wave's ahead.  (Steps on the way, and both launches for
+// one token: one 79 us, two 80, three 83, four 88; 16 tokens: 785, 786, 791, 794.)  The tokens
+// of a tile are cast into shared memory when its first item comes.
+constexpr int kUpThreads = 512, kUpWaves = kUpThreads / kWave;
 constexpr int kUpShared = 126 * 1024;               // bytes of a CU's 160 KB beside what is declared below
 constexpr int kUpOut = 32;                          // outputs of an item
 
@@ -214,48 +214,66 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
     // Blocks go to the 8 chiplets in turn: neighbouring runs to the blocks of one.
     const int64_t b = (blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8) * (kUpWaves / kTeam) + team;
     const int64_t runs = static_cast<int64_t>(gridDim.x) * (kUpWaves / kTeam);
-    const int64_t begin = items * b / runs, end = items * (b + 1) / runs;
+    const int begin = static_cast<int>(items * b / runs), end = static_cast<int>(items * (b + 1) / runs);
     if (begin == end) return;
     // A wave's steps of an item: inputs 128 (wave + kTeam i) .. + 127.
     const int steps = (H / 128 + kTeam - 1) / kTeam;
 
     // The loading side.  Past its end a wave asks for its last step again.
-    u32x4 w[kUpDeep][4][2];
+    u32x4 w[4][2];
     uint32_t row[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) row[j] = (j % 2 * 16 + i16) * static_cast<uint32_t>(H) + q * 16;
     Buffer from[2];
-    int64_t asking = begin;
-    int ask_step = 0;
+    int tile = begin / columns, column = begin % columns;
+    int ask_step = 0, ask_tile = tile, ask_column = column, ask_left = end - begin;
     auto aim = [&] {
-        const int tile = static_cast<int>(asking / columns), column = static_cast<int>(asking - static_cast<int64_t>(tile) * columns);
-        const int8_t* p = up + (static_cast<int64_t>(uniform(s.expert[tile])) * 2 * F + column * kUpOut) * H;
+        const int8_t* p = up + (static_cast<int64_t>(uniform(s.expert[ask_tile])) * 2 * F + ask_column * kUpOut) * H;
         from[0] = buffer(p, static_cast<int64_t>(kUpOut) * H);
         from[1] = buffer(p + static_cast<int64_t>(F) * H, static_cast<int64_t>(kUpOut) * H);
     };
-    auto load = [&](int buf) {
+    auto load = [&] {
         int at = (wave + ask_step * kTeam) * 128;
         at = at < H ? at : H - 128;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) w[buf][j][half] = load16(from[j / 2], row[j], at + 64 * half);
+            for (int half = 0; half < 2; ++half) w[j][half] = load16(from[j / 2], row[j], at + 64 * half);
         __builtin_amdgcn_sched_barrier(0);
         if (++ask_step == steps) {
-            if (++asking < end) {
+            if (--ask_left > 0) {
                 ask_step = 0;
+                if (++ask_column == columns) {
+                    ask_column = 0;
+                    ++ask_tile;
+                }
                 aim();
             } else {
-                --asking;
+                ask_left = 1;
                 --ask_step;
             }
         }
     };
 
-    // The tile at hand: its slots' tokens, cast.  `ready` runs behind the first loads.
-    int tile = -1, count = 0, first = 0;
+    // The scales of an item's rows, asked for while the item before is finished.
+    f32x4 gs[kSides], us[kSides];
+    auto ask_scales = [&] {
+        const float* ws = up_scales + static_cast<int64_t>(uniform(s.expert[tile])) * 2 * F + column * kUpOut + wave % 2 * 16 + 4 * q;
+#pragma unroll
+        for (int g = 0; g < kSides; ++g) {
+            gs[g] = *reinterpret_cast<const f32x4*>(ws + g * 16);
+            us[g] = *reinterpret_cast<const f32x4*>(ws + F + g * 16);
+        }
+    };
+    // The tile at hand, and its slots' tokens from r0 on, cast.  `ready` runs behind the
+    // first loads.
+    int count = 0, first = 0;
     const uint8_t* mine = nullptr;
+    auto enter = [&] {
+        first = uniform(s.first[tile]);
+        count = uniform(s.first[tile + 1]) - first;
+    };
     auto cast_batch = [&](int r0, auto ready) {
         const u32x4* from_x[kBatch];
 #pragma unroll
@@ -263,7 +281,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
             const int token = uniform(s.order[first + (r0 + r < count ? r0 + r : count - 1)]) / k;
             from_x[r] = reinterpret_cast<const u32x4*>(x + static_cast<int64_t>(token) * H);
         }
-        cast_rows<kThreads, kAlone ? 2 : 1, kBatch>(
+        cast_rows<kThreads, kAlone ? 2 : 1, kBatch, false, kAlone>(
             from_x, H / 16, me, row_room[r0 / kBatch % 2], ready,
             [&](int r, int p, const u32x4& v) {
                 if (r0 + r < count) *reinterpret_cast<u32x4*>(codes + (r0 + r) * stride + p * 16) = v;
@@ -272,29 +290,8 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
                 if (me == 0 && r0 + r < count) x_scale[team][r0 + r] = scale;
             });
     };
-    auto stage = [&](int now, auto ready) {
-        tile = now;
-        first = uniform(s.first[tile]);
-        count = uniform(s.first[tile + 1]) - first;
-        cast_batch(0, ready);
-        for (int r0 = kBatch; r0 < count; r0 += kBatch) cast_batch(r0, [] {});
-        mine = codes + (i16 < count ? i16 : count - 1) * stride + q * 16;
-        if constexpr (kAlone) settle_wave();
-        else __syncthreads();
-    };
 
     i32x4 acc[4] = {};
-    // The scales of an item's rows, asked for while the item before is finished.
-    f32x4 gs[kSides], us[kSides];
-    auto ask_scales = [&](int64_t item) {
-        const int t = static_cast<int>(item / columns), column = static_cast<int>(item - static_cast<int64_t>(t) * columns);
-        const float* ws = up_scales + static_cast<int64_t>(uniform(s.expert[t])) * 2 * F + column * kUpOut + wave % 2 * 16 + 4 * q;
-#pragma unroll
-        for (int g = 0; g < kSides; ++g) {
-            gs[g] = *reinterpret_cast<const f32x4*>(ws + g * 16);
-            us[g] = *reinterpret_cast<const f32x4*>(ws + F + g * 16);
-        }
-    };
     // Four outputs of the lane's slot, from n on, and their largest magnitude so far.
     auto result = [&](const i32x4& gate, const i32x4& other, int g, int n, uint32_t m) {
         const float xs = x_scale[team][i16];
@@ -308,7 +305,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
         return m;
     };
     // The waves' sums of an item, and its results.
-    auto finish = [&](int column) {
+    auto finish = [&] {
         uint32_t m = 0u;
         if constexpr (kAlone) {
             if (i16 < count)
@@ -340,42 +337,51 @@ __global__ __launch_bounds__(kUpThreads, 2) void moe_up_i8_kernel(const uint16_t
     };
 
     aim();
-    stage(static_cast<int>(begin / columns), [&] {
-        ask_scales(begin);
-#pragma unroll
-        for (int d = 0; d < kUpDeep; ++d) load(d);
+    enter();
+    cast_batch(0, [&] {
+        ask_scales();
+        load();
     });
-    int64_t item = begin;
-    int column = static_cast<int>(begin % columns), step = 0;
-    const int total = static_cast<int>(end - begin) * steps;
-    for (int g = 0; g < total; g += kUpDeep)
+    // (The code is kept short: it comes from memory anew in every call.  53 KB of it, with two
+    // steps and these casts in each, against 21: 1 token, 1 of 16 experts, 2560 -> 384, 25 / 21
+    // us; 8 of 256, 7168 -> 2048, 78 / 76; 40 tokens, 7 of 64, 1024 -> 1024, 73 / 70; but 64, 6
+    // of 64, 4096 -> 1024, 184 / 186.)
+    int r0 = kBatch;                                // of a tile that is entered anew 0
+    for (int left = end - begin;;) {
+        if (column == 0 || r0 > 0) {
+            if (r0 == 0) {
+                if constexpr (kAlone) settle_wave();        // the last tile's codes are read
+                enter();
+            }
+            for (; r0 < count; r0 += kBatch) cast_batch(r0, [] {});
+            r0 = 0;
+            mine = codes + (i16 < count ? i16 : count - 1) * stride + q * 16;
+            if constexpr (kAlone) settle_wave();
+            else __syncthreads();
+        }
+        int step = 0;
+        do {
+            const int at = (wave + step * kTeam) * 128;
+            if (at < H) {
 #pragma unroll
-        for (int d = 0; d < kUpDeep; ++d) {
-            if (g + d < total) {
-                if (step == 0 && column == columns) {
-                    column = 0;
-                    if constexpr (kAlone) settle_wave();    // the last tile's codes are read
-                    stage(tile + 1, [] {});
-                }
-                const int at = (wave + step * kTeam) * 128;
-                if (at < H) {
+                for (int half = 0; half < 2; ++half) {
+                    const u32x4 t = *reinterpret_cast<const u32x4*>(mine + at + 64 * half);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const u32x4 t = *reinterpret_cast<const u32x4*>(mine + at + 64 * half);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[d][j][half]),
-                                                                           __builtin_bit_cast(i32x4, t), acc[j], 0, 0, 0);
-                    }
-                }
-                if (++step == steps) {
-                    finish(column++);
-                    step = 0;
-                    ask_scales(item + 1 < end ? ++item : item);
+                    for (int j = 0; j < 4; ++j)
+                        acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[j][half]),
+                                                                       __builtin_bit_cast(i32x4, t), acc[j], 0, 0, 0);
                 }
             }
-            load(d);
+            load();
+        } while (++step < steps);
+        finish();
+        if (--left == 0) break;
+        if (++column == columns) {
+            column = 0;
+            ++tile;
         }
+        ask_scales();
+    }
 }
 
 // ---- down ----------------------------------------------------------------------------

@@ -110,8 +110,9 @@ struct RowPieces {
 };
 
 // Codes and scales of kRows rows, handed to to(row, piece, codes) and scale(row, s).
-// `ready` runs behind the first loads.
-template <int kThreads, int kPieces, int kRows, bool kOnce = false, typename Ready, typename To, typename Scale>
+// `ready` runs behind the first loads.  kWhole: a row has kThreads * kPieces pieces at most.
+template <int kThreads, int kPieces, int kRows, bool kOnce = false, bool kWhole = false, typename Ready, typename To,
+          typename Scale>
 __device__ __forceinline__ void cast_rows(const u32x4* const (&rows)[kRows], int pieces, int thread,
                                           uint32_t (&room)[kRows][kThreads / kWave], Ready ready, To to, Scale scale) {
     constexpr int kStep = kThreads * kPieces;
@@ -122,7 +123,7 @@ __device__ __forceinline__ void cast_rows(const u32x4* const (&rows)[kRows], int
     ready();
 #pragma unroll
     for (int r = 0; r < kRows; ++r) m[r] = v[r].most(m[r]);
-    for (int base = kStep; base < pieces; base += kStep)
+    for (int base = kStep; !kWhole && base < pieces; base += kStep)
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             v[r].load(rows[r], pieces, base, thread);
@@ -144,8 +145,8 @@ __device__ __forceinline__ void cast_rows(const u32x4* const (&rows)[kRows], int
     for (int r = 0; r < kRows; ++r) {
         const Cast c = cast_of(m[r]);
         scale(r, c.scale);
-        for (int base = 0; base < pieces; base += kStep) {
-            if (pieces > kStep) v[r].load(rows[r], pieces, base, thread);
+        for (int base = 0; base < (kWhole ? 1 : pieces); base += kStep) {
+            if (!kWhole && pieces > kStep) v[r].load(rows[r], pieces, base, thread);
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int p = base + i * kThreads + thread;
