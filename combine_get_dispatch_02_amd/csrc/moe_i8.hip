@@ -424,7 +424,10 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
     const float* __restrict__ topk_weights, int T, int parts, int k, int E, int H, int F,
     const int8_t* __restrict__ down, const float* __restrict__ down_scales, int chunk_slots, int tile_slots,
     uint16_t* __restrict__ out) {
-    constexpr int kTiles = kRows / 16, kDeep = 4 / kTiles;
+    // A wave has 4 KB on the way: 2 steps of 16 rows, or one of 32.  (8, 4 and 2 KB, both launches,
+    // us: 64 tokens, 8 of 64 experts, 1024 -> 1024, 85, 81, 87; 32, 6 of 64, 4096 -> 1024, 176,
+    // 168, 175; 1, 1 of 16, 2560 -> 384, 22, 20, 20; 16, 8 of 256, 7168 -> 2048, 784, 785, -.)
+    constexpr int kTiles = kRows / 16, kDeep = 2 / kTiles;
     extern __shared__ __align__(16) uint8_t room[];
     const int lane = lane_id(), q = lane / 16, i16 = lane % 16, stride = F + kPad, me = static_cast<int>(threadIdx.x);
     const int wave = uniform(me / kWave), half = chunk_slots * stride;
