@@ -8,10 +8,10 @@
 //         slots with their weights.
 //
 // Bound by reading the weights of the experts that some slot chose, once each: 16 tokens,
-// 8 of 256 experts, 7168 -> 2048 (4.5 GB) 760-790 us, 5.8 TB/s; one token (353 MB) 78 us,
-// 4.5 TB/s (up 48, down 30), of which a launch's start (the slots, the casts, the first
+// 8 of 256 experts, 7168 -> 2048 (4.5 GB) 760-790 us, 5.8 TB/s; one token (353 MB) 76 us,
+// 4.6 TB/s (up 46, down 29), of which a launch's start (the slots, the casts, the first
 // loads) is 6 us or more.  What is left at 64 tokens, 6 of 64 experts, 4096 -> 1024 (805 MB,
-// 186 us, 4.3 TB/s) are the casts of h, 384 rows in every block of down.  The slots are grouped by expert in every block anew (at most kMaxSlots ids), so
+// 184 us, 4.4 TB/s) are the casts of h, 384 rows in every block of down.  The slots are grouped by expert in every block anew (at most kMaxSlots ids), so
 // that no launch has to do it before; the casts too are done by every block for what it
 // needs, out of the caches.  Sums of products are integers, so no order changes a
 // result; each token's slots are added in slot order.
