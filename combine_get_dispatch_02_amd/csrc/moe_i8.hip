@@ -469,7 +469,10 @@ __global__ __launch_bounds__(kDownThreads, kDownThreads / 256) void moe_down_i8_
             const uint32_t bits = larger(larger(m[0], m[1]), larger(m[2], m[3]));
             const float a = __uint_as_float(bits);
             const bool none = bits < 0x04000000u || bits >= 0x7F800000u;    // (127 / a stays finite from 2^-119 on)
-            casts[p] = f32x2{a / 127.0f, none ? 0.0f : 127.0f * __builtin_amdgcn_rcpf(a)};
+            // 127 / a; above 2^60 by way of a * 2^-100, for the reciprocal of more than 2^126 is
+            // below the normal numbers, where the hardware gives 0.
+            const float by = bits > 0x5D800000u ? 0x1p-100f : 1.0f;
+            casts[p] = f32x2{a / 127.0f, none ? 0.0f : 127.0f * by * __builtin_amdgcn_rcpf(a * by)};
         }
         __syncthreads();
         // Pieces of 64 vectors of four of a place's h, place by place, every kCastWaves-th
