@@ -175,22 +175,26 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
 // 16 (or 4) bytes a lane past the registers to shared memory at byte `to` + 16 lane
 // (+ 4 lane).  By hand: the compiler takes any later read of shared memory for one of
 // what such a load writes, and waits for it.  Whoever reads the bytes waits by arrive().
-// (m0 is set here alone: nothing else in these kernels uses it.)
+// The compiler does not see which scalars a load by hand reads, and one that a vector
+// instruction wrote (it may keep scalars in vector lanes) may be read five wait states
+// later at the earliest: s_mov is one, s_nop 3 four.  (With two in all, which is enough only
+// by the order that the compiler happens to choose, the two sizes above take 1 % and 0.3 %
+// less: 1491 against 1507 us, 423 against 424.)
 typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void load_past(uint32_t to, const Words4& from, uint32_t lane_offset, uint32_t offset) {
 #ifdef __HIP_DEVICE_COMPILE__
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(to), "v"(lane_offset), "s"(from), "s"(offset)
-                 : "memory");
+                 : "memory", "m0");
 #endif
 }
 __device__ __forceinline__ void load_past4(uint32_t to, const Words4& from, uint32_t lane_offset) {
 #ifdef __HIP_DEVICE_COMPILE__
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(to), "v"(lane_offset), "s"(from)
-                 : "memory");
+                 : "memory", "m0");
 #endif
 }
 // Where shared memory `p` lies in the block's.
@@ -354,10 +358,11 @@ __device__ __forceinline__ void tile_item(const Call& c, const Item& it, const F
                     for (int t = 0; t < kT; ++t) read_b(u, t, next);
                 }
             }
-            // One every second product, or where there are few in turn.
+            // One every second product (of 16, behind the four that have reads beside
+            // them), or where there are few in turn.
 #pragma unroll
             for (int g = ask0; g < ask1; ++g)
-                if ((kT > 2 ? (g - ask0) * 2 : (g - ask0) % (4 * kT)) == m)
+                if ((kT > 3 ? (g - ask0) * 2 + 4 : kT > 2 ? (g - ask0) * 2 : (g - ask0) % (4 * kT)) == m)
                     ask<kSilu>(f, g, at_ring + (q == 0 ? next : from), wave);
             __builtin_amdgcn_sched_barrier(0);
         }
