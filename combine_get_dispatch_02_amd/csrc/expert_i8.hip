@@ -164,8 +164,8 @@ __global__ __launch_bounds__(kThreads, 2) void stream_i8_kernel(Call c) {
 // A lane holds row l % 32 of either operand, and inputs 32 u + 16 (l / 32) .. + 15 in step
 // u of a stage's four.
 //
-// 256 experts with 128 rows on average, 7168 -> 2 x 2048 (7.9 GB): 1.44-1.50 ms, 5.3-5.5
-// TB/s.  64 with 768, 4096 -> 2 x 1024: 410-450 us, 1.8-2.0 POP/s; half of its cycles are
+// 256 experts with 128 rows on average, 7168 -> 2 x 2048 (7.9 GB): 1.45-1.51 ms, 5.2-5.4
+// TB/s.  64 with 768, 4096 -> 2 x 1024: 420-450 us, 1.8-2.0 POP/s; half of its cycles are
 // the matrix unit's, at the 1.5-1.7 GHz that the card's power leaves (a loop of products
 // alone runs at 3.0-3.2 POP/s), and what nothing hides are the results (an exponential
 // and a reciprocal each: 10 of some 100 thousand cycles an item).  Stages of 64 inputs in

@@ -7,14 +7,23 @@
 //   down  casts h, multiplies it with the experts' down rows, and adds each token's
 //         slots with their weights.
 //
-// Bound by reading the weights of the experts that some slot chose, once each: 16 tokens,
-// 8 of 256 experts, 7168 -> 2048 (4.5 GB) 760-790 us, 5.8 TB/s; one token (353 MB) 76 us,
-// 4.6 TB/s (up 46, down 29), of which a launch's start (the slots, the casts, the first
-// loads) is 6 us or more.  What is left at 64 tokens, 6 of 64 experts, 4096 -> 1024 (805 MB,
-// 184 us, 4.4 TB/s) are the casts of h, 384 rows in every block of down.  The slots are grouped by expert in every block anew (at most kMaxSlots ids), so
-// that no launch has to do it before; the casts too are done by every block for what it
-// needs, out of the caches.  Sums of products are integers, so no order changes a
-// result; each token's slots are added in slot order.
+// Where experts have few slots each, bound by reading the weights of those that some slot
+// chose: 16 tokens, 8 of 256 experts, 7168 -> 2048 (4.5 GB) 760-790 us, 5.8 TB/s; one token
+// (353 MB) 76 us, 4.6 TB/s (up 46, down 29), of which a launch's start (the slots, the
+// casts, the first loads) is 6 us or more.  What is left at 64 tokens, 6 of 64 experts, 4096 ->
+// 1024 (805 MB, 184-201 us, 4.0-4.4 TB/s) are the casts of h, 384 rows in every block of down.
+//
+// Weights are read once for every tile of up to 16 slots of an expert (fewer in up where
+// rows are long: 15 at 8192 inputs, 7 at 16384), in down for every part of the tokens too,
+// from the second time on mostly out of the caches; and every block of down casts h of
+// all its slots.  So many slots an expert cost more than their weights: 64 tokens, 8 of 8
+// experts, 2048 -> 1408 (70 MB, 13 us at 5.2 TB/s) 82 us, 8 of 16, 4096 -> 1408 (278 MB, 53 us)
+// 169; by dispatch, products, cast, products and combine 54 and 86.
+//
+// The slots are grouped by expert in every block anew (at most kMoeMaxSlots ids), so that
+// no launch has to do it before; the casts too are done by every block for what it needs,
+// out of the caches.  Sums of products are integers, so no order changes a result; each
+// token's slots are added in slot order.
 #include "moe_launch.h"
 #include "quant_i8.h"
 #include "stream_i8.h"
@@ -23,8 +32,9 @@ namespace ep {
 namespace {
 
 // ---- the slots by expert -------------------------------------------------------------
-// Tiles of up to `most` slots of one expert, an expert's in order of the slots: every
-// block finds the same, and both launches the same places.
+// Tiles of up to `most` slots of one expert, an expert's in order of the slots.  Blocks that
+// group the same slots find the same places, but the two launches, and parts of the
+// tokens, each have their own: what goes from up to down is held by slot.
 struct Slots {
     int tiles;
     int32_t* expert;                                // [tiles]

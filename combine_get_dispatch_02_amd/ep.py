@@ -910,7 +910,8 @@ def ep_moe_i8(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[to
     [T, k] (None: all 1), with the experts' weights in 8-bit integers: up_i8
     [E, 2F, H] (gate rows first) with up_scales [E, 2F], down_i8 [E, H, F] with
     down_scales [E, H].  Larger batches go through ep_dispatch_i8,
-    ep_expert_linear_i8, ep_quantize_i8, ep_expert_linear_i8 and ep_combine."""
+    ep_expert_linear_i8, ep_quantize_i8, ep_expert_linear_i8 and ep_combine, which
+    are also faster where experts have more than about 8 slots each."""
     us, ds = up_i8.shape, down_i8.shape
     if x.dim() != 2 or len(us) != 3 or len(ds) != 3:
         raise ValueError("x must be [T, H], up_i8 [E, 2F, H] and down_i8 [E, H, F]")

@@ -445,7 +445,8 @@ int ep_combine_backward(const void* grad_out, const void* expert_out, int64_t nu
  * Epilogue.  EP_EPILOGUE_NONE: W has out_features rows.
  * EP_EPILOGUE_SILU_MUL: W has 2*out_features rows, first the gate's, then the
  * up projection's, and y = bf16(silu(gate) * up) with gate and up kept in
- * fp32; silu(v) = v / (1 + exp(-v)).
+ * fp32; silu(v) = v / (1 + exp(-v)), by the hardware's exponential and
+ * reciprocal; below v = -87.3, where |silu| is under 2^-119, it is 0.
  *
  *   x           [num_rows, in_features]     bf16  in (16-byte aligned)
  *   expert_rows [E+1] or [E]                int32 in
@@ -549,8 +550,12 @@ int ep_expert_linear_i8(const int8_t* x_i8, const float* x_scales, int64_t num_r
 /* ---------------------------------------------------------------------------
  * ep_moe_i8 -- the whole layer for a few tokens (T*k <= EP_MOE_MAX_SLOTS slots) in
  * two launches: what ep_dispatch_i8, ep_expert_linear_i8 (silu_mul), ep_quantize_i8,
- * ep_expert_linear_i8 and ep_combine do in a row, reading the weights of each chosen
- * expert once and keeping what is between them in fp32.  For each slot (t, j) with
+ * ep_expert_linear_i8 and ep_combine do in a row, keeping what is between them in
+ * fp32.  It is made for experts with few slots each, whose weights it reads once;
+ * an expert with more than 16 has them read again for every 16 or fewer.  Against
+ * those five calls it takes 0.7 to 1.1 times as long on the GPU with up to 3 slots an
+ * expert, 0.8 to 1.2 with 4 to 8, 1 to 1.5 with 16 and 1.5 to 2.3 with 64; at F = 16384
+ * 1.4 with 4, 2 with 8 and 8 with 64.  For each slot (t, j) with
  * expert e = topk_idx[t, j]:
  *   xq, xs = cast of x[t]
  *   h  = silu(gate) * up, gate and up = sum(xq * w) * (xs * up_scales[e]) (fp32)
